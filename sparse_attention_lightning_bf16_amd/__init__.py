@@ -21,3 +21,19 @@ from .ops import (  # noqa: F401
     topk_bf16,
     v4_lighting_indexer,
 )
+from .rotary_ops import (  # noqa: F401
+    Rotary,
+    RotaryFunction,
+    rotary,
+    rotary_frequencies,
+    rotate_indexer_inputs,
+)
+from .kv8_ops import (  # noqa: F401
+    KV8Cache,
+    kv8_cache,
+    kv8_append,
+    kv8_attention,
+    kv8_attention_workspace_bytes,
+    kv8_token_weights,
+    kv8_evict,
+)

@@ -15,10 +15,13 @@ LIX_ERR_LAUNCH = -5
 LIX_FUSED_TOPK_MAX = 2048
 LIX_NOALLOC_SCRATCH_BYTES = 64 << 20
 
-# Symbols exported by liblix.so, with their C signatures (include/lix.h).
+# Symbols exported by liblix.so, with their C signatures (include/lix.h, lix_rotary.h, lix_kv8.h).
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _LL = ctypes.c_longlong
+_F = ctypes.c_float
+LIX_BF16, LIX_FP16, LIX_FP32 = 0, 1, 2
+LIX_ROTARY_HALF, LIX_ROTARY_INTERLEAVED = 0, 1
 SIGNATURES = {
     "lix_status_string": (ctypes.c_char_p, [_I]),
     "lix_version": (_I, []),
@@ -37,6 +40,18 @@ SIGNATURES = {
     "lix_indexer_backward_workspace_bytes": (_LL, [_I, _I, _I, _I, _I, _I]),
     "lix_indexer_backward_noalloc": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P,
                                           _P]),
+    "lix_rotary": (_I, [_P, _LL, _LL, _LL, _P, _LL, _LL, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P, _LL, _LL,
+                        _LL, _P]),
+    "lix_kv8_append": (_I, [_P, _LL, _LL, _LL, _P, _LL, _LL, _LL, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _I,
+                            _P, _P, _P]),
+    "lix_kv8_attention": (_I, [_P, _LL, _LL, _LL, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P,
+                               _I, _F, _P, _I, _P, _P, _P, _LL, _P]),
+    "lix_kv8_attention_workspace_bytes": (_LL, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "lix_kv8_token_weights": (_I, [_P, _LL, _LL, _LL, _I, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _P, _I,
+                                   _F, _P, _P, _I, _I, _P]),
+    "lix_kv8_evict": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P,
+                           _LL, _P]),
+    "lix_kv8_evict_workspace_bytes": (_LL, [_I, _I, _I, _I, _I, _I]),
 }
 
 _lib = None

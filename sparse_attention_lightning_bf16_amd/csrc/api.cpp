@@ -6,31 +6,22 @@
 // device check.
 #include <stdint.h>
 
-#include <initializer_list>
-
 #include <hip/hip_runtime_api.h>
 
 #include "lix.h"
 #include "launch.h"
+#include "validate.h"
 
 namespace {
+
+using lix::aligned;
+using lix::check_device;
+using lix::fits;
+using lix::launch_status;
 
 constexpr int kVersion = 100;   // 0.1.0
 
 bool is_pow2_le128(int h) { return h >= 1 && h <= 128 && (h & (h - 1)) == 0; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Element counts must stay far inside int64 and the kernels' 32-bit grid limits.
-bool fits(long long a, long long b, long long c = 1, long long d = 1) {
-    const long long lim = 1LL << 40;
-    long long x = a;
-    for (long long f : {b, c, d}) {
-        if (f <= 0 || x > lim / f) return false;
-        x *= f;
-    }
-    return true;
-}
 
 // One workgroup per row or per query block: the row count must fit a 1-D grid.
 bool rows_fit(int B, int S) { return (long long)B * S <= (1LL << 30); }
@@ -52,25 +43,6 @@ int check_dims_v4(int B, int S, int Skv, int H, int D, int ratio, const int32_t*
 bool fused_fits(int Skv, int H, int D, int topk) {
     return topk >= 1 && topk <= LIX_FUSED_TOPK_MAX && Skv <= lix::kFusedMaxSkv && lix::fused_supported(H, D, topk);
 }
-
-// Every pointer must be device (or managed) memory of the current device.
-int check_device(std::initializer_list<const void*> ptrs) {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess) return LIX_ERR_DEVICE;
-    for (const void* p : ptrs) {
-        if (p == nullptr) continue;
-        hipPointerAttribute_t attr;
-        if (hipPointerGetAttributes(&attr, p) != hipSuccess) {
-            (void)hipGetLastError();
-            return LIX_ERR_DEVICE;
-        }
-        if (attr.type != hipMemoryTypeDevice && attr.type != hipMemoryTypeManaged) return LIX_ERR_DEVICE;
-        if (attr.device != dev) return LIX_ERR_DEVICE;
-    }
-    return LIX_OK;
-}
-
-int launch_status(hipError_t e) { return e == hipSuccess ? LIX_OK : LIX_ERR_LAUNCH; }
 
 // The backward's limits: heads <= 64, 32 < index_dim <= 128, a key row of G in LDS.
 int check_dims_backward(int B, int S, int Skv, int H, int D, int ratio, const int32_t* ks, const int32_t* ke,

@@ -1,0 +1,116 @@
+// Internal launch interface between the C ABI (api_rotary.cpp, api_kv8.cpp)
+// and the kernels of rotary positions and of the 8-bit cache.  Arguments have
+// been validated by the caller; launchers only enqueue.  Plain C++.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+#include "lix_rotary.h"
+
+namespace lix {
+
+struct RotaryArgs {
+    const void* x;
+    long x_s0, x_s1, x_sh;
+    const int32_t* positions;
+    long p_s0, p_s1;
+    const double* inv_freq;
+    int N0, N1, H, D, rot, start, layout;
+    float scale;
+    int inverse, dtype;
+    void* out;
+    long o_s0, o_s1, o_sh;
+    hipStream_t stream;
+};
+hipError_t launch_rotary(const RotaryArgs& p);
+
+// The cache as a kernel sees it.
+struct KV8Pages {
+    uint8_t* k;               // e4m3 [num_pages, Hkv, page, D]
+    uint8_t* v;
+    float* k_scale;           // fp32 [num_pages, Hkv]
+    float* v_scale;
+    int num_pages, page_shift;   // page = 1 << page_shift tokens
+    int Hkv, D;
+    const int32_t* table;     // [B, max_pages]
+    int max_pages;
+    const int32_t* lens;      // [B]
+};
+
+struct AppendArgs {
+    const void* x[2];         // k, v
+    long sb[2], ss[2], sh[2];
+    int dtype, B, S;
+    KV8Pages c;
+    const int32_t* new_lens;  // [B] or null
+    hipStream_t stream;
+};
+hipError_t launch_kv8_append(const AppendArgs& p);
+
+struct QueryArgs {
+    const void* q;
+    long sb, ss, sh;
+    int dtype, B, S, Hq, G;   // G = Hq / Hkv
+    const int32_t* q_start;   // [B] or null
+    const int32_t* q_lens;    // [B] or null
+    int ratio;
+    float scale_log2;         // scale * log2(e)
+};
+
+struct AttendArgs {
+    QueryArgs q;
+    KV8Pages c;
+    const int32_t* indices;   // [B, S, topk] or null
+    int topk;
+    void* out;
+    float* lse;
+    float* workspace;
+    hipStream_t stream;
+};
+// How lix_kv8_attention splits its work: rows per wave (16 each) and parts
+// of each sequence (or index list).
+struct AttendPlan {
+    int tiles;                // 16-row tiles of a wave
+    int row_tiles;            // waves for the rows of one (sequence, key head) or query
+    int parts;                // parts of the keys
+    long tasks;               // (sequence, key head[, query]) groups
+    long workspace_bytes;
+};
+AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pages, int topk);
+hipError_t launch_kv8_attention(const AttendArgs& p, const AttendPlan& plan);
+
+struct WeighArgs {
+    QueryArgs q;
+    KV8Pages c;
+    const float* lse;
+    float* weights;
+    int width, accumulate;
+    hipStream_t stream;
+};
+hipError_t launch_kv8_token_weights(const WeighArgs& p);
+
+struct EvictArgs {
+    KV8Pages c;
+    int B;
+    const float* weights;
+    int width;
+    const int32_t* new_table;
+    int new_max_pages;
+    int keep, recent, sinks;
+    int32_t* new_lens;
+    int32_t* kept;
+    float* new_weights;
+    void* workspace;
+    hipStream_t stream;
+};
+// Byte offsets of the parts of lix_kv8_evict's workspace; middle: tokens
+// selected by weight for each row at most.
+struct EvictLayout {
+    long begin, end, scores, indices, total;
+    int middle;
+};
+EvictLayout evict_layout(int B, int Hkv, int width, int keep, int recent, int sinks);
+hipError_t launch_kv8_evict(const EvictArgs& p, const EvictLayout& layout);
+
+}  // namespace lix

@@ -308,7 +308,8 @@ def topk_bf16(scores, topk):
     return out, idx
 
 
-def v4_lighting_indexer(index_q, index_k, weights, compress_ratio, topk, topk_indices=None):
+def v4_lighting_indexer(index_q, index_k, weights, compress_ratio, topk, topk_indices=None, rotary=None,
+                        q_positions=None, k_positions=None):
     """The pages' main entry point (the misspelt name is the pages' own).
 
     Without topk_indices: scoring + top-k, returns (scores, indices): the streaming kernel for
@@ -319,6 +320,15 @@ def v4_lighting_indexer(index_q, index_k, weights, compress_ratio, topk, topk_in
     directly (lix_indexer_scores_at; equal bit for bit to gathering the
     materialized logits), returns scores.  Both go through V4IndexerFunction,
     so the scores carry gradients to index_q, index_k and weights.
+
+    rotary (a Rotary): index_q and index_k come without their positions, which are put in first
+    (rotate_indexer_inputs): query t at t and compressed key s at s * compress_ratio, unless
+    q_positions [S, B] (or [S]) and k_positions [Skv, B] (or [Skv]) int32 are given.
     """
+    if rotary is not None:
+        from .rotary_ops import rotate_indexer_inputs
+        index_q, index_k = rotate_indexer_inputs(index_q, index_k, compress_ratio, rotary, q_positions, k_positions)
+    elif q_positions is not None or k_positions is not None:
+        raise ValueError("q_positions and k_positions need rotary")
     scores, indices = V4IndexerFunction.apply(index_q, index_k, weights, compress_ratio, topk, topk_indices)
     return (scores, indices) if topk_indices is None else scores
