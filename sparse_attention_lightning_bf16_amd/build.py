@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblix.so")
 SOURCES = ["api.cpp", "limits.cpp", "score.hip", "topk.hip", "fused.hip", "sparse.hip", "backward.hip",
            "api_rotary.cpp", "rotary.hip", "api_kv8.cpp", "limits_kv8.cpp", "kv8_append.hip", "kv8_attention.hip",
-           "kv8_weights.hip"]
+           "kv8_prompt.hip", "kv8_weights.hip"]
 # Units whose MFMA accumulators may live in AGPRs (more than 256 registers of
 # accumulators and operands at one wave per SIMD).
 AGPR_SOURCES = {"backward.hip"}

@@ -34,6 +34,9 @@ typedef float f32x2v __attribute__((ext_vector_type(2)));
 struct QBf16 {
     typedef __bf16 elem;
     typedef bf16x8 frag;
+    // Attention weights are rounded to one fp16 (11 bits): below what an
+    // output of 8 bits shows.
+    static constexpr bool kTwoWeights = false;
     static __device__ __forceinline__ f32x4 mfma(const frag& a, const frag& b, const f32x4& c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
@@ -45,6 +48,10 @@ struct QBf16 {
 struct QFp16 {
     typedef _Float16 elem;
     typedef f16x8 frag;
+    // An output of 11 bits would show one rounding of the weights to 11 bits
+    // (1.48 times the error of its own rounding, measured): they are held as
+    // the sum of two fp16, a second product with the remainder.
+    static constexpr bool kTwoWeights = true;
     static __device__ __forceinline__ f32x4 mfma(const frag& a, const frag& b, const f32x4& c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }

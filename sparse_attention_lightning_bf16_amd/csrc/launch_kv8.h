@@ -68,17 +68,19 @@ struct AttendArgs {
     float* workspace;
     hipStream_t stream;
 };
-// How lix_kv8_attention splits its work: rows per wave (16 each) and parts
-// of each sequence (or index list).
+// How lix_kv8_attention splits its work.
 struct AttendPlan {
+    int waves;                // of a workgroup that shares its keys through LDS; 0: every wave by itself
     int tiles;                // 16-row tiles of a wave
-    int row_tiles;            // waves for the rows of one (sequence, key head) or query
+    int row_tiles;            // such workgroups (or waves) for the rows of one (sequence, key head) or query
     int parts;                // parts of the keys
     long tasks;               // (sequence, key head[, query]) groups
     long workspace_bytes;
 };
 AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pages, int topk);
 hipError_t launch_kv8_attention(const AttendArgs& p, const AttendPlan& plan);
+// The part of launch_kv8_attention for plans with waves > 0, before any joining.
+hipError_t launch_kv8_tiles(const AttendArgs& p, const AttendPlan& plan);
 
 struct WeighArgs {
     QueryArgs q;

@@ -5,10 +5,11 @@
 
 namespace lix {
 
-// A wave takes 32 rows where there are more than 16 and their accumulators
-// leave room for two waves per SIMD (D <= 128), else 16.  Where the rows
-// make fewer waves than fill the card (8 for each of 256 CUs), the keys are
-// split into parts of at least 128 keys.
+// Rows to a wave: 32 where their accumulators leave room for two waves per
+// SIMD (D <= 128) and there are more than 16, else 16.  Many rows: workgroups
+// of 4 waves that share the conversion of their keys (2 where a query's heads
+// fill no more).  Where the rows make fewer waves than fill the card (8 for
+// each of 256 CUs), the keys are split into parts of at least 128 keys.
 AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pages, int topk) {
     constexpr long kWaves = 2048, kPartKeys = 128, kMaxParts = 256;
     const int G = Hq / Hkv;
@@ -16,9 +17,12 @@ AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_p
     const long keys = topk > 0 ? topk : (long)max_pages * page;
     AttendPlan p{};
     p.tiles = rows > 16 && D <= 128 ? 2 : 1;
-    p.row_tiles = (int)((rows + 16 * p.tiles - 1) / (16 * p.tiles));
+    if (topk > 0) p.waves = rows <= 16 ? 0 : rows <= 2 * 16 * p.tiles ? 2 : 4;
+    else p.waves = rows > 8 * 16 * p.tiles ? 8 : rows > 64 ? 4 : 0;
+    const long group = 16L * p.tiles * (p.waves > 0 ? p.waves : 1);
+    p.row_tiles = (int)((rows + group - 1) / group);
     p.tasks = (long)B * Hkv * (topk > 0 ? S : 1);
-    const long waves = p.tasks * p.row_tiles;
+    const long waves = p.tasks * p.row_tiles * (p.waves > 0 ? p.waves : 1);
     long parts = (kWaves + waves - 1) / waves;
     const long most = (keys + kPartKeys - 1) / kPartKeys;
     if (parts > most) parts = most;

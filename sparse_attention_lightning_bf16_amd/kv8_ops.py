@@ -33,23 +33,33 @@ def kv8_cache(num_pages, kv_heads, page, head_dim, device="cuda"):
     return KV8Cache(codes(), codes(), scales(), scales())
 
 
+def _is(x, dtype, ndim, dev):
+    return (isinstance(x, torch.Tensor) and x.dtype is dtype and x.ndim == ndim and x.get_device() == dev
+            and x.is_contiguous())
+
+
 def _cache(cache, table, lens):
+    """Checks a cache and its tables; the shape of the codes.  One pass of cheap tests first: the calls of a
+    decoding step last about as long on the host as on the GPU."""
     k, v, ks, vs = cache
-    _need(k, "cache.k", torch.float8_e4m3fn, 4)
-    _need(v, "cache.v", torch.float8_e4m3fn, 4)
-    _need(ks, "cache.k_scale", torch.float32, 2)
-    _need(vs, "cache.v_scale", torch.float32, 2)
-    _need(table, "block_table", torch.int32, 2)
-    _need(lens, "kv_lens", torch.int32, 1)
-    if v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != k.shape[:2]:
+    dev = k.get_device()
+    if not (dev >= 0 and _is(k, torch.float8_e4m3fn, 4, dev) and _is(v, torch.float8_e4m3fn, 4, dev)
+            and _is(ks, torch.float32, 2, dev) and _is(vs, torch.float32, 2, dev)
+            and _is(table, torch.int32, 2, dev) and _is(lens, torch.int32, 1, dev)):
+        _need(k, "cache.k", torch.float8_e4m3fn, 4)
+        _need(v, "cache.v", torch.float8_e4m3fn, 4)
+        _need(ks, "cache.k_scale", torch.float32, 2)
+        _need(vs, "cache.v_scale", torch.float32, 2)
+        _need(table, "block_table", torch.int32, 2)
+        _need(lens, "kv_lens", torch.int32, 1)
+        raise ValueError("the cache, block_table and kv_lens must be on the same device")
+    shape = k.shape
+    if v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
         raise ValueError("the cache must hold k and v [num_pages, kv_heads, page, head_dim] and scales "
                          "[num_pages, kv_heads]")
     if lens.shape[0] != table.shape[0]:
         raise ValueError("block_table and kv_lens must have one row per sequence")
-    dev = k.device
-    if v.device != dev or ks.device != dev or vs.device != dev or table.device != dev or lens.device != dev:
-        raise ValueError("the cache, block_table and kv_lens must be on the same device")
-    return k.shape
+    return shape
 
 
 def _rows(x, name, batch, device):
@@ -68,11 +78,12 @@ def _rows(x, name, batch, device):
 
 
 def _per_sequence(x, name, lens):
-    if x is not None:
+    if x is None:
+        return None
+    if not _is(x, torch.int32, 1, lens.get_device()) or x.shape[0] != lens.shape[0]:
         _need(x, name, torch.int32, 1)
-        if x.shape != lens.shape or x.device != lens.device:
-            raise ValueError(f"{name} must have one entry per sequence, on the cache's device")
-    return _ptr(x)
+        raise ValueError(f"{name} must have one entry per sequence, on the cache's device")
+    return x.data_ptr()
 
 
 def kv8_append(cache, k, v, block_table, kv_lens, new_lens=None):
@@ -130,7 +141,7 @@ def kv8_attention(q, cache, block_table, kv_lens, q_start=None, q_lens=None, com
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
         _need(workspace, "workspace", torch.uint8, 1)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    out = torch.empty_like(q, memory_format=torch.contiguous_format)
     lse = torch.empty((B, S, Hq), dtype=torch.float32, device=q.device)
     st = lib.lix_kv8_attention(
         q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), _DTYPES[q.dtype], B, S, Hq, heads, dim,

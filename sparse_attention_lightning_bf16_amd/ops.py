@@ -16,7 +16,9 @@ def _ptr(t):
 
 
 def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle of torch.cuda.current_stream(device), without building the Stream object around it
+    # (0.1 us instead of 2 on the host)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _need(t, name, dtype, ndim):
