@@ -128,13 +128,20 @@ long long lix_kv8_attention_workspace_bytes(int B, int S, int Hq, int Hkv, int D
  *
  *   lse      fp32 [B, S, Hq], as lix_kv8_attention gave it for these queries
  *   weights  fp32 [B, Hkv, width], width >= max_pages * page
+ *   workspace  lix_kv8_token_weights_workspace_bytes bytes, 256-byte aligned
+ *            (NULL where that is 0); contents unspecified before and after
  */
 int lix_kv8_token_weights(const void* q, long long q_sb, long long q_ss, long long q_sh, int dtype,
                           int B, int S, int Hq, int Hkv, int D,
                           const void* k_pages, const float* k_scales, int num_pages, int page,
                           const int32_t* block_table, int max_pages, const int32_t* kv_lens,
                           const int32_t* q_start, const int32_t* q_lens, int compress_ratio, float scale,
-                          const float* lse, float* weights, int width, int accumulate, hipStream_t stream);
+                          const float* lse, float* weights, int width, int accumulate,
+                          void* workspace, long long workspace_bytes, hipStream_t stream);
+
+/* Workspace of lix_kv8_token_weights for these sizes: the sums of the parts that many queries are split into where
+ * there are few keys, 0 where they are not; -1 for sizes that the call does not take.  Pure host function. */
+long long lix_kv8_token_weights_workspace_bytes(int B, int S, int Hq, int Hkv, int D, int page, int max_pages);
 
 /*
  * lix_kv8_evict - keeps the tokens with the largest weights, in new pages.

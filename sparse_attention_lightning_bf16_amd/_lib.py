@@ -48,7 +48,8 @@ SIGNATURES = {
                                _I, _F, _P, _I, _P, _P, _P, _LL, _P]),
     "lix_kv8_attention_workspace_bytes": (_LL, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "lix_kv8_token_weights": (_I, [_P, _LL, _LL, _LL, _I, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _P, _I,
-                                   _F, _P, _P, _I, _I, _P]),
+                                   _F, _P, _P, _I, _I, _P, _LL, _P]),
+    "lix_kv8_token_weights_workspace_bytes": (_LL, [_I, _I, _I, _I, _I, _I, _I]),
     "lix_kv8_evict": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P,
                            _LL, _P]),
     "lix_kv8_evict_workspace_bytes": (_LL, [_I, _I, _I, _I, _I, _I]),

@@ -170,18 +170,24 @@ int lix_kv8_token_weights(const void* q, long long q_sb, long long q_ss, long lo
                           int Hq, int Hkv, int D, const void* k_pages, const float* k_scales, int num_pages, int page,
                           const int32_t* block_table, int max_pages, const int32_t* kv_lens, const int32_t* q_start,
                           const int32_t* q_lens, int compress_ratio, float scale, const float* lse, float* weights,
-                          int width, int accumulate, hipStream_t stream) {
+                          int width, int accumulate, void* workspace, long long workspace_bytes,
+                          hipStream_t stream) {
     if (!q || !k_pages || !k_scales || !block_table || !kv_lens || !lse || !weights) return LIX_ERR_NULL;
     int st = check_queries(dtype, B, S, Hq, Hkv, D, compress_ratio, scale);
     if (st == LIX_OK) st = check_cache(num_pages, page, Hkv, D, B, max_pages);
     if (st == LIX_OK) st = check_strides(q_sb, B, q_ss, S, q_sh, Hq);
     if (st != LIX_OK) return st;
     if (width < (long long)max_pages * page) return LIX_ERR_SHAPE;
-    if (!fits(B, Hkv, width) || !grid_fits((double)B * Hkv * max_pages)) return LIX_ERR_UNSUPPORTED;
+    const WeighPlan plan = weigh_plan(B, S, Hq, Hkv, D, page, max_pages);
+    if (!fits(B, Hkv, width) || !grid_fits((double)B * Hkv * max_pages * plan.parts)) return LIX_ERR_UNSUPPORTED;
+    if (plan.workspace_bytes > 0 && workspace == nullptr) return LIX_ERR_NULL;
+    if (workspace_bytes < plan.workspace_bytes) return LIX_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(k_scales, 4) || !aligned(block_table, 4) ||
-        !aligned(kv_lens, 4) || !aligned(q_start, 4) || !aligned(q_lens, 4) || !aligned(lse, 4) || !aligned(weights, 4))
+        !aligned(kv_lens, 4) || !aligned(q_start, 4) || !aligned(q_lens, 4) || !aligned(lse, 4) || !aligned(weights, 4) ||
+        !aligned(workspace, 256))
         return LIX_ERR_UNSUPPORTED;
-    st = check_device({q, k_pages, k_scales, block_table, kv_lens, q_start, q_lens, lse, weights});
+    st = check_device({q, k_pages, k_scales, block_table, kv_lens, q_start, q_lens, lse, weights,
+                       plan.workspace_bytes > 0 ? workspace : nullptr});
     if (st != LIX_OK) return st;
     WeighArgs a{};
     a.q = queries_of(q, q_sb, q_ss, q_sh, dtype, B, S, Hq, Hkv, q_start, q_lens, compress_ratio, scale);
@@ -190,8 +196,18 @@ int lix_kv8_token_weights(const void* q, long long q_sb, long long q_ss, long lo
     a.weights = weights;
     a.width = width;
     a.accumulate = accumulate;
+    a.cap = (long)max_pages * page;
+    a.parts = plan.parts;
+    a.workspace = static_cast<float*>(workspace);
     a.stream = stream;
-    return launch_status(launch_kv8_token_weights(a));
+    return launch_status(launch_kv8_token_weights(a, plan));
+}
+
+long long lix_kv8_token_weights_workspace_bytes(int B, int S, int Hq, int Hkv, int D, int page, int max_pages) {
+    if (check_cache(1, page, Hkv, D, B, max_pages) != LIX_OK ||
+        check_queries(LIX_BF16, B, S, Hq, Hkv, D, 1, 1.0f) != LIX_OK)
+        return -1;
+    return weigh_plan(B, S, Hq, Hkv, D, page, max_pages).workspace_bytes;
 }
 
 long long lix_kv8_evict_workspace_bytes(int B, int Hkv, int width, int keep, int recent, int sinks) {

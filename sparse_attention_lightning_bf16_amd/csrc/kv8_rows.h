@@ -302,34 +302,6 @@ struct Task {
     bool live;
 };
 
-template <int NT, bool SEL>
-__device__ __forceinline__ Task wave_task(const AttendArgs& a, const AttendPlan& plan) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    Task k;
-    const long pairs = (long)a.q.B * a.c.Hkv;
-    const long block = blockIdx.x;
-    const long pair = block % pairs;
-    long u = block / pairs * 4 + wave;             // (row tile, part) of the pair, part fastest
-    const int groups = SEL ? a.q.S : 1;
-    const long units = (long)groups * plan.row_tiles * plan.parts;
-    k.live = u < units;
-    k.b = (int)(pair / a.c.Hkv);
-    k.kvh = (int)(pair % a.c.Hkv);
-    k.part = (int)(u % plan.parts);
-    u /= plan.parts;
-    if (SEL) {
-        k.row0 = (int)(u % plan.row_tiles) * 16 * NT;
-        k.t = (int)(u / plan.row_tiles);
-        k.rows = a.q.G;
-    } else {
-        // late rows see the most keys: they go first
-        k.row0 = (plan.row_tiles - 1 - (int)u) * 16 * NT;
-        k.t = 0;
-        k.rows = a.q.S * a.q.G;
-    }
-    return k;
-}
-
 // Query and head of row r of the wave's group.
 template <bool SEL>
 __device__ __forceinline__ void row_of(const AttendArgs& a, const Task& k, int r, int& t, int& head) {

@@ -2,12 +2,20 @@
 //     w[s] = sum over the rows (queries x heads of a key head) that see s of
 //            2^(scale log2(e) k_scale (q . code[s]) - log2(e) lse)
 //
-// A wave owns 16 KT keys of one key head: their codes are converted once to
-// operand fragments that stay in registers, and the rows pass by, 16 at a
-// time.  Keys are the rows of the product (kv8_core.h), so a lane adds up its
-// own keys over all rows it sees and the sum over the 16 row columns is taken
-// once at the end: no atomics, the same order on every call.  One query: bound
-// by reading the key codes; many: by the exponentials.
+// Keys are the rows of the product (kv8_core.h): a lane adds up its own keys
+// over all rows that pass, and the sum over the 16 row columns is taken once,
+// at the end.  No atomics, the same order on every call.
+//
+// Many rows: a wave keeps 64 keys (32 for D = 256) as operand fragments in
+// registers and the rows pass by, 16 at a time, the next 16 on their way.  The
+// four waves of a workgroup have neighbouring keys, so that they read the same
+// rows at about the same time.  The rows of a key range are split into parts
+// where there are too few ranges; their sums go to the workspace and are added
+// by a second kernel.  Bound by the exponentials and the products.
+//
+// One tile of 16 rows: the rows stay in registers and the keys pass by, 16 at
+// a time per step and two steps ahead, 64 steps' pages looked up at once.  Bound
+// by reading the key codes.
 #include <hip/hip_runtime.h>
 
 #include "kv8_core.h"
@@ -18,15 +26,35 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// v summed over the 16 lanes of a row group (l % 16), in every lane.
+__device__ __forceinline__ float row_sum(float v) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xf, 0xf, true));      // row_ror:8
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xf, 0xf, true));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x122, 0xf, 0xf, true));
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x121, 0xf, 0xf, true));
+}
+
+// ---------------------------------------------------------------- many rows
+
+// 16 rows and their -log2(e) lse.
+template <class Q, int D>
+struct RowTile {
+    typename Q::frag f[D / 32];
+    float lse;
+};
+
 template <class Q, int D, int KT>
 __global__ __launch_bounds__(256, 2) void kv8_weights_kernel(WeighArgs a) {
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const long pairs = (long)a.q.B * a.c.Hkv;
     const long pair = blockIdx.x % pairs;
+    long u = blockIdx.x / pairs;
+    const int part = (int)(u % a.parts);
+    u /= a.parts;
     const int b = (int)(pair / a.c.Hkv), kvh = (int)(pair % a.c.Hkv);
     const int len = cached_len(a.c, b);
-    const long s_first = (blockIdx.x / pairs * 4 + wave) * (16L * KT);
+    const long s_first = (u * 4 + wave) * (16L * KT);
     if (s_first >= len) return;
     const int s0 = (int)s_first;
     const int shift = a.c.page_shift;
@@ -45,95 +73,238 @@ __global__ __launch_bounds__(256, 2) void kv8_weights_kernel(WeighArgs a) {
         const uint8_t* p = a.c.k + ((at << shift) + (s & ((1 << shift) - 1)) + (lane & 15)) * D + 16 * g;
         c[h] = exists[h] ? a.c.k_scale[at] * a.q.scale_log2 : 0.0f;
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(p + 64 * u);
-            key[h][2 * u] = key_frag<Q>(w[0], w[1]);
-            key[h][2 * u + 1] = key_frag<Q>(w[2], w[3]);
+        for (int u4 = 0; u4 < D / 64; ++u4) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(p + 64 * u4);
+            key[h][2 * u4] = key_frag<Q>(w[0], w[1]);
+            key[h][2 * u4 + 1] = key_frag<Q>(w[2], w[3]);
         }
     }
+
+    // Rows [first, all_from) see some of the keys, [all_from, rows) all of them;
+    // rows behind the last query are left out.
+    const int G = a.q.G;
+    const int queries = a.q.q_lens ? min(max(a.q.q_lens[b], 0), a.q.S) : a.q.S;
+    const int rows = queries * G;
+    int first = 0, all_from = 0;
+    if (a.q.q_start != nullptr) {
+        const long start = a.q.q_start[b];
+        first = (int)min(max(((long)s0 + 1) * a.q.ratio - 1 - start, 0L), (long)queries) * G;
+        all_from = (int)min(max(((long)s0 + 16 * KT) * a.q.ratio - 1 - start, 0L), (long)queries) * G;
+    }
+    if (s0 + 16 * KT > len) all_from = rows;                    // keys behind the sequence
+    const int tiles = (rows - first + 15) / 16;
+    const int per_part = (tiles + a.parts - 1) / a.parts;
+    const int t_lo = min(part * per_part, tiles), t_hi = min(t_lo + per_part, tiles);
 
     f32x4 sum[KT];
 #pragma unroll
     for (int h = 0; h < KT; ++h) sum[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const typename Q::elem* q = static_cast<const typename Q::elem*>(a.q.q) + b * a.q.sb + 16 * g;
-    const int rows = a.q.S * a.q.G;
-    // rows before the first query that sees this wave's first key add nothing
-    int first = 0;
-    if (a.q.q_start != nullptr) {
-        const long t = ((long)s0 + 1) * a.q.ratio - 1 - a.q.q_start[b];
-        first = (int)min(max(t, 0L), (long)a.q.S) * a.q.G;
-    }
-    for (int r0 = first; r0 < rows; r0 += 16) {
-        const int r = min(r0 + (lane & 15), rows - 1);
-        const int t = r / a.q.G, head = kvh * a.q.G + r - t * a.q.G;
-        typename Q::frag f[D / 32];
+    if (t_lo < t_hi) {
+        const typename Q::elem* q = static_cast<const typename Q::elem*>(a.q.q) + b * a.q.sb + 16 * g;
+        // query and head of this lane's row of the tile that is loaded next
+        const int r_first = first + 16 * t_lo + (lane & 15);
+        int t = r_first / G, h_of = r_first - t * G;
+        const int step_t = 16 / G, step_h = 16 - step_t * G;
+        auto load = [&](RowTile<Q, D>& x) {
+            const bool in = t < queries;
+            const int tt = in ? t : queries - 1, head = kvh * G + (in ? h_of : 0);
+            const typename Q::elem* at = q + tt * a.q.ss + head * a.q.sh;
 #pragma unroll
-        for (int ks = 0; ks < D / 32; ++ks)
-            f[ks] = *reinterpret_cast<const typename Q::frag*>(q + t * a.q.ss + head * a.q.sh + 64 * (ks / 2) +
-                                                               8 * (ks & 1));
-        const float lse = a.lse[((long)b * a.q.S + t) * a.q.Hq + head];
-        int vis = r0 + (lane & 15) < rows ? visible_tokens(a.q, b, t, len) : 0;
-        if (lse == neg_inf()) vis = 0;
-        const float base = -lse * kLog2e;
-        const bool edge = __any(vis < s0 + 16 * KT) || s0 + 16 * KT > len;
-#pragma unroll
-        for (int h = 0; h < KT; ++h) {
-            f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks) x = Q::mfma(key[h][ks], f[ks], x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c[h], base));
-                if (edge) p = s0 + 16 * h + 4 * g + i < vis ? p : 0.0f;
-                sum[h][i] += p;
+            for (int ks = 0; ks < D / 32; ++ks)
+                x.f[ks] = *reinterpret_cast<const typename Q::frag*>(at + 64 * (ks / 2) + 8 * (ks & 1));
+            x.lse = a.lse[((long)b * a.q.S + tt) * a.q.Hq + head];
+            t += step_t;
+            h_of += step_h;
+            const bool wrap = h_of >= G;
+            t += wrap ? 1 : 0;
+            h_of -= wrap ? G : 0;
+        };
+        auto add = [&](const RowTile<Q, D>& x, int i) {
+            // a row whose lse is -inf gives nothing, whatever its scores are
+            const int r0 = first + 16 * i;
+            const bool edge = r0 < all_from || r0 + 16 > rows || __any(x.lse == neg_inf());
+            const float base = -x.lse * kLog2e;
+            int vis = 0;
+            if (edge) {
+                const int r = r0 + (lane & 15);
+                vis = r < rows && x.lse != neg_inf() ? visible_tokens(a.q, b, r / G, len) - s0 : 0;
             }
+#pragma unroll
+            for (int h = 0; h < KT; ++h) {
+                f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int ks = 0; ks < D / 32; ++ks) y = Q::mfma(key[h][ks], x.f[ks], y);
+                f32x4 p;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[j], c[h], base));
+                if (edge) {
+                    int here = 4 * g;
+                    asm volatile("" : "+v"(here));              // the masks stay inside the branch
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) p[j] = 16 * h + here + j < vis ? p[j] : 0.0f;
+                }
+                sum[h] += p;
+            }
+        };
+        RowTile<Q, D> one, two;
+        load(one);
+        for (int i = t_lo; i < t_hi; i += 2) {
+            if (i + 1 < t_hi) load(two);
+            add(one, i);
+            if (i + 2 < t_hi) load(one);
+            if (i + 1 < t_hi) add(two, i + 1);
         }
     }
-    // over the 16 columns; lane l % 16 == i writes key 4 g + i
 #pragma unroll
     for (int h = 0; h < KT; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float v = sum[h][i];
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o);
+            const float v = exists[h] ? row_sum(sum[h][i]) : 0.0f;
             const int s = s0 + 16 * h + 4 * g + i;
-            if ((lane & 15) == i && s < len) {
+            if ((lane & 15) != i || s >= len) continue;
+            if (a.parts > 1) {
+                a.workspace[(part * pairs + pair) * a.cap + s] = v;
+            } else {
                 float* w = a.weights + pair * a.width + s;
-                const float got = exists[h] ? v : 0.0f;
-                *w = a.accumulate ? *w + got : got;
+                *w = a.accumulate ? *w + v : v;
             }
         }
 }
 
-template <class Q, int D>
-hipError_t launch(const WeighArgs& a) {
-    const long cap = (long)a.c.max_pages << a.c.page_shift;
+// The parts' sums of each token, in order.
+__global__ __launch_bounds__(256) void kv8_weights_join_kernel(WeighArgs a) {
     const long pairs = (long)a.q.B * a.c.Hkv;
-    // 64 keys a wave read each row of queries least often; with one row tile
-    // there is nothing to share, and 32 keys a wave spread further
-    auto go = [&](auto kernel, long keys) {
-        const long grid = pairs * ((cap + 4 * keys - 1) / (4 * keys));
-        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, a.stream, a);
+    const long pair = blockIdx.x % pairs;
+    const int s = (int)(blockIdx.x / pairs) * 256 + threadIdx.x;
+    if (s >= cached_len(a.c, (int)(pair / a.c.Hkv))) return;
+    float v = 0.0f;
+    for (int p = 0; p < a.parts; ++p) v += a.workspace[(p * pairs + pair) * a.cap + s];
+    float* w = a.weights + pair * a.width + s;
+    *w = a.accumulate ? *w + v : v;
+}
+
+// ---------------------------------------------------------------- one tile of rows
+
+
+template <class Q, int D>
+__global__ __launch_bounds__(256, 2) void kv8_weights_few_kernel(WeighArgs a, int range) {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const long pairs = (long)a.q.B * a.c.Hkv;
+    const long pair = blockIdx.x % pairs;
+    const int b = (int)(pair / a.c.Hkv), kvh = (int)(pair % a.c.Hkv);
+    const int len = cached_len(a.c, b);
+    const long first = (blockIdx.x / pairs * 4 + wave) * (long)range;
+    if (first >= len) return;
+    const int lo = (int)first, hi = min(lo + range, len);
+    const int shift = a.c.page_shift, G = a.q.G, rows = a.q.S * G;
+
+    // lane e: entry e of 16 keys, its row of the cache and scale
+    const int token = lo + 16 * lane;
+    const int pid = token < hi ? a.c.table[(long)b * a.c.max_pages + (token >> shift)] : -1;
+    const bool there = pid >= 0 && pid < a.c.num_pages;
+    const long at = (long)(there ? pid : 0) * a.c.Hkv + kvh;
+    const int row = there ? (int)((at << shift) + (token & ((1 << shift) - 1))) : 0;
+    const float scale = there ? a.c.k_scale[at] * a.q.scale_log2 : 0.0f;
+    const uint64_t good = __ballot(there);
+
+    const int r = lane & 15, rc = min(r, rows - 1);
+    const int t = rc / G, head = kvh * G + rc - t * G;
+    const typename Q::elem* q =
+        static_cast<const typename Q::elem*>(a.q.q) + b * a.q.sb + t * a.q.ss + head * a.q.sh + 16 * g;
+    typename Q::frag f[D / 32];
+    const uint32_t off = (lane & 15) * D + 16 * g;
+    struct Codes {
+        u32x4 w[2][D / 64];
     };
-    if (a.q.S * a.q.G > 16 && D <= 128) go(kv8_weights_kernel<Q, D, 4>, 64);
-    else go(kv8_weights_kernel<Q, D, 2>, 32);
+    auto load = [&](Codes& x, int i) {             // keys 32 i .. of the range
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t* p = a.c.k + (long)__builtin_amdgcn_readlane(row, 2 * i + h) * D;
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) x.w[h][u] = *reinterpret_cast<const u32x4*>(p + (off + 64u * u));
+        }
+    };
+    const int steps = (hi - lo + 31) / 32;
+    Codes one, two;
+    load(one, 0);
+    if (steps > 1) load(two, 1);
+#pragma unroll
+    for (int ks = 0; ks < D / 32; ++ks) f[ks] = *reinterpret_cast<const typename Q::frag*>(q + 64 * (ks / 2) + 8 * (ks & 1));
+    const float lse = a.lse[((long)b * a.q.S + t) * a.q.Hq + head];
+    const int vis = r < rows && lse != neg_inf() ? visible_tokens(a.q, b, t, len) : 0;
+    const float base = -lse * kLog2e;
+    int least = vis;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) least = min(least, __shfl_xor(least, o));
+    least = __builtin_amdgcn_readfirstlane(least);
+
+    float* w = a.weights + pair * a.width;
+    auto add = [&](const Codes& x, int i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int s0 = lo + 32 * i + 16 * h;
+            const float c = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale), 2 * i + h));
+            f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) {
+                y = Q::mfma(key_frag<Q>(x.w[h][u][0], x.w[h][u][1]), f[2 * u], y);
+                y = Q::mfma(key_frag<Q>(x.w[h][u][2], x.w[h][u][3]), f[2 * u + 1], y);
+            }
+            f32x4 p;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[j], c, base));
+            if (s0 + 16 > least) {
+                const bool is = good >> (2 * i + h) & 1;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p[j] = is && s0 + 4 * g + j < vis ? p[j] : 0.0f;
+            } else if (!(good >> (2 * i + h) & 1)) {
+                p = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = row_sum(p[j]);
+            const int s = s0 + 4 * g + (lane & 3);
+            const float v = lane & 2 ? (lane & 1 ? p[3] : p[2]) : (lane & 1 ? p[1] : p[0]);
+            if ((lane & 15) < 4 && s < hi) w[s] = a.accumulate ? w[s] + v : v;
+        }
+    };
+    for (int i = 0; i < steps; i += 2) {
+        add(one, i);
+        if (i + 2 < steps) load(one, i + 2);
+        if (i + 1 < steps) add(two, i + 1);
+        if (i + 3 < steps) load(two, i + 3);
+    }
+}
+
+template <class Q, int D>
+hipError_t launch(const WeighArgs& a, const WeighPlan& plan) {
+    const long pairs = (long)a.q.B * a.c.Hkv;
+    auto groups = [&](long keys) { return dim3((unsigned)(pairs * ((a.cap + 4 * keys - 1) / (4 * keys)) * plan.parts)); };
+    if (plan.range > 0) {
+        hipLaunchKernelGGL((kv8_weights_few_kernel<Q, D>), groups(plan.range), dim3(256), 0, a.stream, a, plan.range);
+        return hipGetLastError();
+    }
+    constexpr int KT = D <= 128 ? 4 : 2;
+    hipLaunchKernelGGL((kv8_weights_kernel<Q, D, KT>), groups(16 * KT), dim3(256), 0, a.stream, a);
+    if (plan.parts > 1)
+        hipLaunchKernelGGL(kv8_weights_join_kernel, dim3((unsigned)(pairs * ((a.cap + 255) / 256))), dim3(256), 0,
+                           a.stream, a);
     return hipGetLastError();
 }
 
 template <class Q>
-hipError_t launch_dim(const WeighArgs& a) {
+hipError_t launch_dim(const WeighArgs& a, const WeighPlan& plan) {
     switch (a.c.D) {
-        case 64: return launch<Q, 64>(a);
-        case 128: return launch<Q, 128>(a);
-        default: return launch<Q, 256>(a);
+        case 64: return launch<Q, 64>(a, plan);
+        case 128: return launch<Q, 128>(a, plan);
+        default: return launch<Q, 256>(a, plan);
     }
 }
 
 }  // namespace
 
-hipError_t launch_kv8_token_weights(const WeighArgs& a) {
-    return a.q.dtype == LIX_BF16 ? launch_dim<QBf16>(a) : launch_dim<QFp16>(a);
+hipError_t launch_kv8_token_weights(const WeighArgs& a, const WeighPlan& plan) {
+    return a.q.dtype == LIX_BF16 ? launch_dim<QBf16>(a, plan) : launch_dim<QFp16>(a, plan);
 }
 
 }  // namespace lix

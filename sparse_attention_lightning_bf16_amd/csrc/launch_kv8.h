@@ -68,12 +68,13 @@ struct AttendArgs {
     float* workspace;
     hipStream_t stream;
 };
+constexpr int kMaxParts = 256;
 // How lix_kv8_attention splits its work.
 struct AttendPlan {
-    int waves;                // of a workgroup that shares its keys through LDS; 0: every wave by itself
+    int waves;                // of a workgroup that shares its keys through LDS; 0: that shares its rows
     int tiles;                // 16-row tiles of a wave
-    int row_tiles;            // such workgroups (or waves) for the rows of one (sequence, key head) or query
-    int parts;                // parts of the keys
+    int row_tiles;            // workgroups for the rows of one (sequence, key head) or query
+    int parts;                // parts of the keys, at most kMaxParts
     long tasks;               // (sequence, key head[, query]) groups
     long workspace_bytes;
 };
@@ -88,9 +89,19 @@ struct WeighArgs {
     const float* lse;
     float* weights;
     int width, accumulate;
+    long cap;                 // tokens of a table row
+    int parts;                // of the rows (WeighPlan)
+    float* workspace;         // [parts, B, Hkv, cap], parts > 1
     hipStream_t stream;
 };
-hipError_t launch_kv8_token_weights(const WeighArgs& p);
+// How lix_kv8_token_weights splits its work: parts of the rows, or, for one
+// tile of 16 rows, the keys of a wave (range > 0).
+struct WeighPlan {
+    int parts, range;
+    long workspace_bytes;
+};
+WeighPlan weigh_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pages);
+hipError_t launch_kv8_token_weights(const WeighArgs& p, const WeighPlan& plan);
 
 struct EvictArgs {
     KV8Pages c;

@@ -7,11 +7,15 @@ namespace lix {
 
 // Rows to a wave: 32 where their accumulators leave room for two waves per
 // SIMD (D <= 128) and there are more than 16, else 16.  Many rows: workgroups
-// of 4 waves that share the conversion of their keys (2 where a query's heads
-// fill no more).  Where the rows make fewer waves than fill the card (8 for
-// each of 256 CUs), the keys are split into parts of at least 128 keys.
+// of 8 or 4 waves that share the conversion of their keys (2 where a query's
+// heads fill no more), each wave with its own rows.  Few: workgroups of 4 waves
+// that share the rows and take turns at the keys.
+//
+// Where the rows make too few workgroups, the keys are split into parts of at
+// least 512 keys: for many rows until the card is full (2048 waves), for few
+// until there are 1024 workgroups, two for each place on the card.
 AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pages, int topk) {
-    constexpr long kWaves = 2048, kPartKeys = 128, kMaxParts = 256;
+    constexpr long kWaves = 2048, kGroups = 1024, kPartKeys = 512;
     const int G = Hq / Hkv;
     const long rows = topk > 0 ? G : (long)S * G;
     const long keys = topk > 0 ? topk : (long)max_pages * page;
@@ -22,13 +26,37 @@ AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_p
     const long group = 16L * p.tiles * (p.waves > 0 ? p.waves : 1);
     p.row_tiles = (int)((rows + group - 1) / group);
     p.tasks = (long)B * Hkv * (topk > 0 ? S : 1);
-    const long waves = p.tasks * p.row_tiles * (p.waves > 0 ? p.waves : 1);
-    long parts = (kWaves + waves - 1) / waves;
+    const long groups = p.tasks * p.row_tiles;
+    const long wanted = p.waves > 0 ? kWaves / p.waves : kGroups;
+    long parts = (wanted + groups - 1) / groups;
     const long most = (keys + kPartKeys - 1) / kPartKeys;
     if (parts > most) parts = most;
     if (parts > kMaxParts) parts = kMaxParts;
     p.parts = (int)parts;
     p.workspace_bytes = parts > 1 ? p.tasks * parts * rows * (D + 2) * 4 : 0;
+    return p;
+}
+
+// One tile of rows: ranges of 1024 keys to a wave (64 lookups of 16), shorter
+// ones down to 64 where that leaves fewer than 4096 waves.  More rows: 256 keys
+// (128 for D = 256) to a workgroup, the rows in parts until there are 1024
+// workgroups, at least eight tiles of 16 rows to a part.
+WeighPlan weigh_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pages) {
+    const long cap = (long)max_pages * page, pairs = (long)B * Hkv, rows = (long)S * (Hq / Hkv);
+    WeighPlan p{};
+    p.parts = 1;
+    if (rows <= 16) {
+        p.range = 1024;
+        while (p.range > 64 && pairs * ((cap + p.range - 1) / p.range) < 4096) p.range /= 2;
+        return p;
+    }
+    const long keys = D <= 128 ? 256 : 128;
+    const long groups = pairs * ((cap + keys - 1) / keys);
+    long parts = (1024 + groups - 1) / groups;
+    const long most = (rows + 127) / 128;
+    if (parts > most) parts = most;
+    p.parts = (int)parts;
+    p.workspace_bytes = parts > 1 ? parts * pairs * cap * 4 : 0;
     return p;
 }
 

@@ -180,11 +180,14 @@ def kv8_token_weights(q, cache, block_table, kv_lens, lse, q_start=None, q_lens=
         _need(out, "out", torch.float32, 3)
         if out.shape[0] != B or out.shape[1] != heads or out.device != q.device:
             raise ValueError(f"out must be [{B}, {heads}, width] on the device of q")
-    st = _lib.load().lix_kv8_token_weights(
+    lib = _lib.load()
+    need = lib.lix_kv8_token_weights_workspace_bytes(B, S, Hq, heads, dim, page, mp)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    st = lib.lix_kv8_token_weights(
         q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), _DTYPES[q.dtype], B, S, Hq, heads, dim,
         cache.k.data_ptr(), cache.k_scale.data_ptr(), pages, page, block_table.data_ptr(), mp, kv_lens.data_ptr(),
         start, lens, int(compress_ratio), scale, lse.data_ptr(), out.data_ptr(), out.shape[2], int(bool(accumulate)),
-        _stream(q.device))
+        _ptr(ws), max(need, 0), _stream(q.device))
     _lib.check(st, "lix_kv8_token_weights")
     return out
 

@@ -93,22 +93,24 @@ QUERY = [
 
 @pytest.mark.parametrize("kw,code", [c for c in COMMON if "s" not in c[0]] + QUERY + [
     (dict(s=(-8, 256, 64)), SHAPE), (dict(s=(512, 256, 68)), UNSUP), (dict(vp=None), NULL), (dict(out=None), NULL),
-    (dict(idx=P, topk=0), SHAPE), (dict(idx=P + 2, topk=4), UNSUP), (dict(out=P + 8), UNSUP), (dict(ws=None), NULL),
-    (dict(ws=P + 16), UNSUP), (dict(ws_bytes=16), SHAPE), (dict(S=4096, mp=1, ws=None, ws_bytes=0), DEVICE),
+    (dict(idx=P, topk=0), SHAPE), (dict(idx=P + 2, topk=4), UNSUP), (dict(out=P + 8), UNSUP), (dict(mp=64, ws=None), NULL),
+    (dict(ws=P + 16), UNSUP), (dict(mp=64, ws_bytes=16), SHAPE), (dict(mp=64), DEVICE),
+    (dict(ws=None, ws_bytes=0), DEVICE),             # one part: no workspace
 ])
 def test_attention_validation(kw, code):
     assert attention_call(**kw) == code
 
 
 def weights_call(q=P, s=(512, 256, 64), dtype=0, B=2, S=1, Hq=4, H=2, D=64, start=None, qlens=None, ratio=1,
-                 scale=0.125, lse=P, w=P, width=256, acc=0, **kw):
+                 scale=0.125, lse=P, w=P, width=256, acc=0, ws=None, ws_bytes=0, **kw):
     c = dict(CACHE, **kw)
     return lx.load().lix_kv8_token_weights(q, *s, dtype, B, S, Hq, H, D, c["kp"], c["ks"], c["np_"], c["page"], c["table"],
-                                           c["mp"], c["lens"], start, qlens, ratio, scale, lse, w, width, acc, None)
+                                           c["mp"], c["lens"], start, qlens, ratio, scale, lse, w, width, acc, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw,code", QUERY + [
-    (dict(w=None), NULL), (dict(width=255), SHAPE), (dict(w=P + 2), UNSUP), (dict(page=20), UNSUP), (dict(D=32), UNSUP),
+    (dict(w=None), NULL), (dict(width=255), SHAPE), (dict(w=P + 2), UNSUP), (dict(page=20), UNSUP), (dict(ws=P + 8), UNSUP),
+    (dict(S=512), NULL), (dict(S=512, ws=P), SHAPE), (dict(S=512, ws=P, ws_bytes=1 << 20), DEVICE), (dict(D=32), UNSUP),
     (dict(), DEVICE),
 ])
 def test_token_weights_validation(kw, code):
@@ -146,6 +148,12 @@ def test_workspace_sizes():
     for bad in ((0, 1, 8, 1, 128, 64, 4), (1, 1, 7, 2, 128, 64, 4), (1, 1, 8, 1, 100, 64, 4), (1, 1, 8, 1, 128, 60, 4),
                 (1, 1, 8, 1, 128, 64, 4, -1)):
         assert f(*bad) == -1
+    w = lx.load().lix_kv8_token_weights_workspace_bytes
+    assert w(2, 1, 16, 1, 128, 64, 8) == 0                   # one tile of rows
+    assert w(64, 64, 64, 64, 128, 64, 64) == 0               # key ranges enough
+    need = w(1, 2048, 32, 4, 128, 64, 64)
+    assert need > 0 and need % (4 * 4096 * 4) == 0
+    assert w(1, 1, 7, 2, 128, 64, 4) == -1 and w(1, 1, 8, 2, 96, 64, 4) == -1
     g = lx.load().lix_kv8_evict_workspace_bytes
     up = lambda x: (x + 255) // 256 * 256   # noqa: E731
     assert g(2, 4, 1000, 300, 50, 10) == 2 * up(8 * 4) + 2 * up(8 * 240 * 4)
