@@ -160,7 +160,8 @@ long long lix_kv8_token_weights_workspace_bytes(int B, int S, int Hq, int Hkv, i
  *   new_lens     int32 [B]             out: min(n, keep)
  *   kept         int32 [B, Hkv, keep]  out: the kept tokens, -1 behind them
  *   new_weights  fp32  [B, Hkv, keep]  out: their weights, 0 behind them
- *   workspace    lix_kv8_evict_workspace_bytes bytes, 256-byte aligned
+ *   workspace    lix_kv8_evict_workspace_bytes bytes, 256-byte aligned (NULL
+ *                where that is 0)
  * LIX_ERR_SHAPE: a size < 1, sinks or recent < 0, sinks + recent > keep, a
  * width or new_max_pages that is too small, or a smaller workspace.
  */
@@ -171,8 +172,10 @@ int lix_kv8_evict(void* k_pages, void* v_pages, float* k_scales, float* v_scales
                   int keep, int recent, int sinks, int32_t* new_lens, int32_t* kept, float* new_weights,
                   void* workspace, long long workspace_bytes, hipStream_t stream);
 
-/* Workspace of lix_kv8_evict: the selected middle tokens and the rows' ranges; -1 for sizes it does not take. */
-long long lix_kv8_evict_workspace_bytes(int B, int Hkv, int width, int keep, int recent, int sinks);
+/* Workspace of lix_kv8_evict: the selected tokens and ranges of rows beyond 32768 tokens, 0 for tables that hold no
+ * more; -1 for sizes it does not take.  Pure host function. */
+long long lix_kv8_evict_workspace_bytes(int B, int Hkv, int page, int max_pages, int width, int keep, int recent,
+                                        int sinks);
 
 #ifdef __cplusplus
 }

@@ -52,7 +52,7 @@ SIGNATURES = {
     "lix_kv8_token_weights_workspace_bytes": (_LL, [_I, _I, _I, _I, _I, _I, _I]),
     "lix_kv8_evict": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P,
                            _LL, _P]),
-    "lix_kv8_evict_workspace_bytes": (_LL, [_I, _I, _I, _I, _I, _I]),
+    "lix_kv8_evict_workspace_bytes": (_LL, [_I, _I, _I, _I, _I, _I, _I, _I]),
 }
 
 _lib = None

@@ -210,11 +210,12 @@ long long lix_kv8_token_weights_workspace_bytes(int B, int S, int Hq, int Hkv, i
     return weigh_plan(B, S, Hq, Hkv, D, page, max_pages).workspace_bytes;
 }
 
-long long lix_kv8_evict_workspace_bytes(int B, int Hkv, int width, int keep, int recent, int sinks) {
-    if (B <= 0 || Hkv <= 0 || width <= 0 || keep <= 0 || recent < 0 || sinks < 0 || recent > keep ||
+long long lix_kv8_evict_workspace_bytes(int B, int Hkv, int page, int max_pages, int width, int keep, int recent,
+                                        int sinks) {
+    if (check_cache(1, page, Hkv, 64, B, max_pages) != LIX_OK || width <= 0 || keep <= 0 || recent < 0 || sinks < 0 || recent > keep ||
         sinks > keep - recent || !fits(B, Hkv, width) || !fits(B, Hkv, keep) || (long long)B * Hkv > (1LL << 30))
         return -1;
-    return evict_layout(B, Hkv, width, keep, recent, sinks).total;
+    return evict_layout(B, Hkv, (long)max_pages * page, width, keep, recent, sinks).total;
 }
 
 int lix_kv8_evict(void* k_pages, void* v_pages, float* k_scales, float* v_scales, int num_pages, int page, int B,
@@ -223,7 +224,7 @@ int lix_kv8_evict(void* k_pages, void* v_pages, float* k_scales, float* v_scales
                   int sinks, int32_t* new_lens, int32_t* kept, float* new_weights, void* workspace,
                   long long workspace_bytes, hipStream_t stream) {
     if (!k_pages || !v_pages || !k_scales || !v_scales || !block_table || !kv_lens || !weights || !new_table ||
-        !new_lens || !kept || !new_weights || !workspace)
+        !new_lens || !kept || !new_weights)
         return LIX_ERR_NULL;
     int st = check_cache(num_pages, page, Hkv, D, B, max_pages);
     if (st != LIX_OK) return st;
@@ -233,14 +234,15 @@ int lix_kv8_evict(void* k_pages, void* v_pages, float* k_scales, float* v_scales
     if (!fits(B, Hkv, width) || !fits(B, Hkv, keep) || !fits(B, new_max_pages) || (long long)B * Hkv > (1LL << 30) ||
         keep > (1 << 30) || !grid_fits((double)B * Hkv * 2 * ((keep + page - 1) / page)))
         return LIX_ERR_UNSUPPORTED;
-    const EvictLayout ly = evict_layout(B, Hkv, width, keep, recent, sinks);
+    const EvictLayout ly = evict_layout(B, Hkv, (long)max_pages * page, width, keep, recent, sinks);
+    if (ly.total > 0 && workspace == nullptr) return LIX_ERR_NULL;
     if (workspace_bytes < ly.total) return LIX_ERR_SHAPE;
     if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_scales, 4) || !aligned(v_scales, 4) ||
         !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(weights, 4) || !aligned(new_table, 4) ||
         !aligned(new_lens, 4) || !aligned(kept, 4) || !aligned(new_weights, 4) || !aligned(workspace, 256))
         return LIX_ERR_UNSUPPORTED;
     st = check_device({k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, weights, new_table, new_lens, kept,
-                       new_weights, workspace});
+                       new_weights, ly.total > 0 ? workspace : nullptr});
     if (st != LIX_OK) return st;
     EvictArgs a{};
     a.c = pages_of(k_pages, v_pages, k_scales, v_scales, num_pages, page, Hkv, D, block_table, max_pages, kv_lens);

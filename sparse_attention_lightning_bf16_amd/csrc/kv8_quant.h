@@ -18,16 +18,12 @@ __device__ __forceinline__ float page_scale(float top) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Four values / scale as e4m3 bytes: round to nearest even, saturating; NaN
-// stays NaN.  The division by a power of two is exact; by another scale it is
-// one correctly rounded fp32 division.
-__device__ __forceinline__ uint32_t e4m3_quad(const float (&x)[4], float scale) {
+// Four values as e4m3 bytes: round to nearest even, saturating; NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3_quad(const float (&x)[4]) {
     float y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float q = x[i] / scale;
-        y[i] = q > kE4M3Max ? kE4M3Max : q < -kE4M3Max ? -kE4M3Max : q;     // NaN compares false twice
-    }
+    for (int i = 0; i < 4; ++i)
+        y[i] = x[i] > kE4M3Max ? kE4M3Max : x[i] < -kE4M3Max ? -kE4M3Max : x[i];     // NaN compares false twice
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
     w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
     return (uint32_t)w;

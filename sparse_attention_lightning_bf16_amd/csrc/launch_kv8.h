@@ -117,13 +117,15 @@ struct EvictArgs {
     void* workspace;
     hipStream_t stream;
 };
-// Byte offsets of the parts of lix_kv8_evict's workspace; middle: tokens
-// selected by weight for each row at most.
+// lix_kv8_evict: whether its rows are selected by the row top-k, the byte
+// offsets of the parts of the workspace that this takes, and the tokens it
+// selects of a row (middle).
 struct EvictLayout {
+    bool by_topk;
     long begin, end, scores, indices, total;
     int middle;
 };
-EvictLayout evict_layout(int B, int Hkv, int width, int keep, int recent, int sinks);
+EvictLayout evict_layout(int B, int Hkv, long cap, int width, int keep, int recent, int sinks);
 hipError_t launch_kv8_evict(const EvictArgs& p, const EvictLayout& layout);
 
 }  // namespace lix

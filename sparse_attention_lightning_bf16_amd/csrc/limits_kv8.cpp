@@ -38,7 +38,7 @@ AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_p
 }
 
 // One tile of rows: ranges of 1024 keys to a wave (64 lookups of 16), shorter
-// ones down to 64 where that leaves fewer than 4096 waves.  More rows: 256 keys
+// ones down to 64 where that leaves fewer than 8192 waves.  More rows: 256 keys
 // (128 for D = 256) to a workgroup, the rows in parts until there are 1024
 // workgroups, at least eight tiles of 16 rows to a part.
 WeighPlan weigh_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pages) {
@@ -47,7 +47,7 @@ WeighPlan weigh_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pag
     p.parts = 1;
     if (rows <= 16) {
         p.range = 1024;
-        while (p.range > 64 && pairs * ((cap + p.range - 1) / p.range) < 4096) p.range /= 2;
+        while (p.range > 64 && pairs * ((cap + p.range - 1) / p.range) < 8192) p.range /= 2;
         return p;
     }
     const long keys = D <= 128 ? 256 : 128;
@@ -60,10 +60,12 @@ WeighPlan weigh_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pag
     return p;
 }
 
-EvictLayout evict_layout(int B, int Hkv, int width, int keep, int recent, int sinks) {
+EvictLayout evict_layout(int B, int Hkv, long cap, int width, int keep, int recent, int sinks) {
     auto up = [](long x) { return (x + 255) & ~255L; };
     const long rows = (long)B * Hkv;
     EvictLayout ly{};
+    ly.by_topk = cap > 32768;
+    if (!ly.by_topk) return ly;
     // a row with more than keep tokens has more than keep - recent - sinks in the
     // middle, and width covers them all
     const int middle = keep - recent - sinks;

@@ -208,11 +208,11 @@ def kv8_evict(cache, block_table, kv_lens, weights, new_block_table, keep, recen
     if new_block_table.shape[0] != B or new_block_table.device != cache.k.device:
         raise ValueError("new_block_table must have one row per sequence, on the cache's device")
     lib = _lib.load()
-    need = lib.lix_kv8_evict_workspace_bytes(B, heads, weights.shape[2], keep, recent, sinks)
+    need = lib.lix_kv8_evict_workspace_bytes(B, heads, page, mp, weights.shape[2], keep, recent, sinks)
     if need < 0:
         raise _lib.LixError(_lib.LIX_ERR_SHAPE, "lix_kv8_evict_workspace_bytes")
     dev = cache.k.device
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
     new_lens = torch.empty(B, dtype=torch.int32, device=dev)
     kept = torch.empty((B, heads, keep), dtype=torch.int32, device=dev)
     new_weights = torch.empty((B, heads, keep), dtype=torch.float32, device=dev)
@@ -220,6 +220,6 @@ def kv8_evict(cache, block_table, kv_lens, weights, new_block_table, keep, recen
         cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), pages, page, B,
         heads, dim, block_table.data_ptr(), mp, kv_lens.data_ptr(), weights.data_ptr(), weights.shape[2],
         new_block_table.data_ptr(), new_block_table.shape[1], keep, recent, sinks, new_lens.data_ptr(),
-        kept.data_ptr(), new_weights.data_ptr(), ws.data_ptr(), need, _stream(dev))
+        kept.data_ptr(), new_weights.data_ptr(), _ptr(ws), need, _stream(dev))
     _lib.check(st, "lix_kv8_evict")
     return new_lens, kept, new_weights

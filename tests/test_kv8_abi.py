@@ -126,12 +126,12 @@ def evict_call(B=2, H=2, D=64, w=P, width=256, new=P, nmp=2, keep=100, recent=10
 
 @pytest.mark.parametrize("kw,code", [
     (dict(w=None), NULL), (dict(new=None), NULL), (dict(nl=None), NULL), (dict(kept=None), NULL), (dict(nw=None), NULL),
-    (dict(ws=None), NULL), (dict(vs=None), NULL),
+    (dict(vs=None), NULL), (dict(mp=1000, width=64000, ws=None), NULL),
     (dict(keep=0), SHAPE), (dict(recent=-1), SHAPE), (dict(sinks=-1), SHAPE), (dict(recent=97), SHAPE),
     (dict(recent=101, sinks=0), SHAPE), (dict(sinks=2147483647), SHAPE), (dict(width=255), SHAPE), (dict(nmp=1), SHAPE),
-    (dict(nmp=0), SHAPE), (dict(ws_bytes=100), SHAPE), (dict(B=-1), SHAPE),
+    (dict(nmp=0), SHAPE), (dict(mp=1000, width=64000, ws_bytes=100), SHAPE), (dict(B=-1), SHAPE),
     (dict(page=24), UNSUP), (dict(D=100), UNSUP), (dict(w=P + 1), UNSUP), (dict(ws=P + 64), UNSUP), (dict(kp=P + 4), UNSUP),
-    (dict(), DEVICE), (dict(recent=96), DEVICE),
+    (dict(), DEVICE), (dict(recent=96), DEVICE), (dict(ws=None, ws_bytes=0), DEVICE),
 ])
 def test_evict_validation(kw, code):
     assert evict_call(**kw) == code
@@ -156,10 +156,11 @@ def test_workspace_sizes():
     assert w(1, 1, 7, 2, 128, 64, 4) == -1 and w(1, 1, 8, 2, 96, 64, 4) == -1
     g = lx.load().lix_kv8_evict_workspace_bytes
     up = lambda x: (x + 255) // 256 * 256   # noqa: E731
-    assert g(2, 4, 1000, 300, 50, 10) == 2 * up(8 * 4) + 2 * up(8 * 240 * 4)
-    assert g(2, 4, 100, 300, 0, 0) == 2 * up(8 * 4) + 2 * up(8 * 100 * 4)
-    assert g(2, 4, 1000, 60, 50, 10) == 2 * up(8 * 4)
-    for bad in ((0, 4, 10, 5, 0, 0), (1, 1, 10, 5, 6, 0), (1, 1, 10, 5, 3, 3), (1, 1, 0, 5, 0, 0), (1, 1, 10, 5, -1, 0)):
+    assert g(2, 4, 64, 512, 32768, 300, 50, 10) == 0         # rows that fit the registers of a workgroup
+    assert g(2, 4, 64, 513, 40000, 300, 50, 10) == 2 * up(8 * 4) + 2 * up(8 * 240 * 4)
+    assert g(2, 4, 64, 513, 40000, 60, 50, 10) == 2 * up(8 * 4)
+    for bad in ((0, 4, 64, 8, 512, 5, 0, 0), (1, 1, 64, 8, 512, 5, 6, 0), (1, 1, 64, 8, 512, 5, 3, 3),
+                (1, 1, 64, 8, 0, 5, 0, 0), (1, 1, 64, 8, 512, 5, -1, 0), (1, 1, 60, 8, 512, 5, 0, 0)):
         assert g(*bad) == -1
 
 
