@@ -312,14 +312,15 @@ struct ListInfo {
     uint32_t ok[2];                    // entries that are there
 };
 
-// One query's list, 16 W entries a tile: half of the waves load and convert
-// its keys, half its values.  Lane e of every wave looks up entry e of the next
-// 64: its token and page while the entries before are used, its row of the cache
-// and scales one tile before they are needed, so that no load waits for
+// One query's list, 32 entries a tile, for two waves: one loads and converts
+// the keys, the other the values, two tiles ahead of the one in use (a gather
+// from L2 takes longer than a tile).  Lane e of both looks up entry e of the
+// next 64: its token and page while the entries before are used, its row of the
+// cache and scales when their codes are to be loaded, so that no load waits for
 // another's address.  FAR: the pages pass 4 GiB, offsets into them take 64 bits.
-template <class Q, int D, int NT, int W, bool FAR>
-__global__ __launch_bounds__(64 * W, 2) void kv8_selected_tiles_kernel(AttendArgs a, AttendPlan plan) {
-    constexpr int KT = 16 * W, kBatch = 64 / KT, VB = D / 16;      // VB: a lane's value codes of one key
+template <class Q, int D, int NT, bool FAR>
+__global__ __launch_bounds__(128, 2) void kv8_selected_tiles_kernel(AttendArgs a, AttendPlan plan) {
+    constexpr int W = 2, KT = 32, VB = D / 16;     // VB: a lane's value codes of one key
     __shared__ Tile<D, KT> tiles[2];
     __shared__ ListInfo infos[2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -387,51 +388,50 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_selected_tiles_kernel(AttendArg
                 return base + x;
         };
 
-        const bool does_keys = wave < W / 2;
-        const int half = does_keys ? wave : wave - W / 2;      // 32 entries of the tile
-        uint32_t code[2 * VB];
-        auto load = [&](int e0) {                  // e0: the tile's first of the 64 entries
-            if (does_keys) {
+        struct Codes {
+            uint32_t w[2 * VB];
+        };
+        auto load = [&](Codes& x, int e0) {        // e0: the tile's first of the 64 entries
+            if (wave == 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint8_t* p = row_at(a.c.k, e0 + 32 * half + 16 * h + (lane & 15), 16 * g);
+                    const uint8_t* p = row_at(a.c.k, e0 + 16 * h + (lane & 15), 16 * g);
 #pragma unroll
                     for (int u = 0; u < D / 64; ++u) {
-                        const u32x4 x = *reinterpret_cast<const u32x4*>(p + 64 * u);
+                        const u32x4 v = *reinterpret_cast<const u32x4*>(p + 64 * u);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) code[VB * h + 4 * u + i] = x[i];
+                        for (int i = 0; i < 4; ++i) x.w[VB * h + 4 * u + i] = v[i];
                     }
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint8_t* p = row_at(a.c.v, e0 + 32 * half + 4 * g + (16 * (j / 4) + j % 4), (lane & 15) * VB);
+                    const uint8_t* p = row_at(a.c.v, e0 + 4 * g + (16 * (j / 4) + j % 4), (lane & 15) * VB);
                     if constexpr (VB == 4) {
-                        code[j] = *reinterpret_cast<const uint32_t*>(p);
+                        x.w[j] = *reinterpret_cast<const uint32_t*>(p);
                     } else if constexpr (VB == 8) {
-                        const uint2 x = *reinterpret_cast<const uint2*>(p);
-                        code[j] = x.x;
-                        code[8 + j] = x.y;
+                        const uint2 v = *reinterpret_cast<const uint2*>(p);
+                        x.w[j] = v.x;
+                        x.w[8 + j] = v.y;
                     } else {
-                        const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+                        const u32x4 v = *reinterpret_cast<const u32x4*>(p);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) code[8 * u + j] = x[u];
+                        for (int u = 0; u < 4; ++u) x.w[8 * u + j] = v[u];
                     }
                 }
             }
         };
-        // converts them into buffer `to`
-        auto store = [&](int e0, int to) {
+        // converts them into buffer `to`; there: which of the tile's entries are
+        auto store = [&](const Codes& x, uint32_t there, int to) {
             Tile<D, KT>& t = tiles[to];
-            if (does_keys) {
+            if (wave == 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int ks = 0; ks < D / 32; ++ks)
-                        t.k[2 * half + h][ks][lane] = __builtin_bit_cast(
-                            u32x4, key_frag<Q>(code[VB * h + 2 * ks], code[VB * h + 2 * ks + 1]));
+                        t.k[h][ks][lane] =
+                            __builtin_bit_cast(u32x4, key_frag<Q>(x.w[VB * h + 2 * ks], x.w[VB * h + 2 * ks + 1]));
             } else {
-                const uint32_t there = (uint32_t)(good >> (e0 + 32 * half));
                 uint32_t ok = ~0u;
                 if (there != ~0u) {
                     ok = 0;
@@ -442,69 +442,75 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_selected_tiles_kernel(AttendArg
                 for (int u = 0; u < D / 64; ++u) {
                     uint32_t v[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = code[8 * u + j];
+                    for (int j = 0; j < 8; ++j) v[j] = x.w[8 * u + j];
                     if (there != ~0u) clear_unit(v, ok);
                     f16x8 f[4];
                     value_frags(v, f);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) t.v[half][4 * u + e][lane] = __builtin_bit_cast(u32x4, f[e]);
+                    for (int e = 0; e < 4; ++e) t.v[0][4 * u + e][lane] = __builtin_bit_cast(u32x4, f[e]);
                 }
             }
         };
+        auto compute = [&](int i) {                // tile i
+            const ListInfo& info = infos[i >> 1 & 1];
+            const float next_ref = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(info.ref)));
+            if (next_ref > w.ref) w.set_ref(next_ref);
+            const int e0 = 32 * (i & 1);
+            Scales<2, true> sc;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 c4 = *reinterpret_cast<const f32x4*>(&info.c[e0 + 16 * h + 4 * g]);
+                const f32x4 r4 = *reinterpret_cast<const f32x4*>(&info.r[e0 + 16 * h + 4 * g]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    sc.c[4 * h + x] = c4[x];
+                    sc.r[4 * h + x] = r4[x];
+                }
+            }
+            const uint32_t there = __builtin_amdgcn_readfirstlane(info.ok[i & 1]);
+            uint32_t ok = ~0u;
+            if (there != ~0u) {
+                ok = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ok |= (there >> key_of(j, g) & 1) << j;
+            }
+            const int none[NT] = {};
+            step<Q, D, NT, 2, true>(w, SharedKeys<Q, D, KT>{tiles[i & 1], 0, lane}, sc, there != ~0u, none, ok, false);
+        };
 
+        // Even tiles pass through `even`, odd ones through `odd`; tile i is used
+        // from buffer i & 1.  held: the entries that are there of the 64 whose
+        // tiles are stored, good: of those whose codes are loaded.
+        const int count = (hi - lo + KT - 1) / KT;
+        Codes even, odd;
         look();
-        load(0);
+        load(even, 0);
+        if (count > 1) load(odd, 32);
         if (wave == 0) inform(infos[0]);
-        store(0, 0);
+        uint64_t held = good;
+        store(even, (uint32_t)held, 0);
+        if (count > 2) {
+            look();
+            load(even, 0);
+        }
         __syncthreads();
-        int cur = 0, t = 0, batch = 0;             // t: the tile's place in its 64 entries
-        for (int s0 = lo; s0 < hi; s0 += KT) {
-            const bool more = s0 + KT < hi;
-            const int next = t + 1 == kBatch ? 0 : t + 1;
-            if (more) {
-                if (next == 0) look();
-                load(next * KT);
+        for (int i = 0; i < count; i += 2) {
+            if (has_rows) compute(i);
+            if (i + 1 < count) store(odd, (uint32_t)(held >> 32), 1);
+            if (i + 3 < count) load(odd, 32);
+            __syncthreads();
+            if (i + 1 >= count) break;
+            if (has_rows) compute(i + 1);
+            if (i + 2 < count) {
+                if (wave == 0) inform(infos[(i + 2) >> 1 & 1]);
+                held = good;
+                store(even, (uint32_t)held, 0);
             }
-            if (has_rows) {
-                const ListInfo& info = infos[batch];
-                const float next_ref = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(info.ref)));
-                if (next_ref > w.ref) w.set_ref(next_ref);
-#pragma unroll
-                for (int p = 0; p < KT / 32; ++p) {
-                    const int e0 = t * KT + 32 * p;
-                    Scales<2, true> sc;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const f32x4 c4 = *reinterpret_cast<const f32x4*>(&info.c[e0 + 16 * h + 4 * g]);
-                        const f32x4 r4 = *reinterpret_cast<const f32x4*>(&info.r[e0 + 16 * h + 4 * g]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            sc.c[4 * h + i] = c4[i];
-                            sc.r[4 * h + i] = r4[i];
-                        }
-                    }
-                    const uint32_t there = __builtin_amdgcn_readfirstlane(info.ok[e0 / 32]);
-                    uint32_t ok = ~0u;
-                    if (there != ~0u) {
-                        ok = 0;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) ok |= (there >> key_of(j, g) & 1) << j;
-                    }
-                    const int none[NT] = {};
-                    step<Q, D, NT, 2, true>(w, SharedKeys<Q, D, KT>{tiles[cur], 2 * p, lane}, sc, there != ~0u, none, ok,
-                                            false);
-                }
-            }
-            if (more) {
-                if (next == 0) {
-                    batch ^= 1;
-                    if (wave == 0) inform(infos[batch]);
-                }
-                store(next * KT, cur ^ 1);
+            if (i + 4 < count) {
+                look();
+                load(even, 0);
             }
             __syncthreads();
-            cur ^= 1;
-            t = next;
         }
     }
     if (has_rows) store_rows<Q, D, NT, true>(a, plan, k, w);
@@ -522,8 +528,7 @@ hipError_t launch(const AttendArgs& a, const AttendPlan& plan) {
     const bool far = ((double)a.c.num_pages * a.c.Hkv * D) * (1 << a.c.page_shift) > 4294967296.0;
     if (!sel && plan.waves == 8) go(kv8_dense_tiles_kernel<Q, D, NT, 8, KT>, 8);
     else if (!sel) go(kv8_dense_tiles_kernel<Q, D, NT, 4, KT>, 4);
-    else if (plan.waves == 4) far ? go(kv8_selected_tiles_kernel<Q, D, NT, 4, true>, 4) : go(kv8_selected_tiles_kernel<Q, D, NT, 4, false>, 4);
-    else far ? go(kv8_selected_tiles_kernel<Q, D, NT, 2, true>, 2) : go(kv8_selected_tiles_kernel<Q, D, NT, 2, false>, 2);
+    else far ? go(kv8_selected_tiles_kernel<Q, D, NT, true>, 2) : go(kv8_selected_tiles_kernel<Q, D, NT, false>, 2);
     return hipGetLastError();
 }
 

@@ -7,11 +7,12 @@
 // at the end.  No atomics, the same order on every call.
 //
 // Many rows: a wave keeps 64 keys (32 for D = 256) as operand fragments in
-// registers and the rows pass by, 16 at a time, the next 16 on their way.  The
-// four waves of a workgroup have neighbouring keys, so that they read the same
-// rows at about the same time.  The rows of a key range are split into parts
-// where there are too few ranges; their sums go to the workspace and are added
-// by a second kernel.  Bound by the exponentials and the products.
+// registers, and the four waves of a workgroup, with neighbouring keys, pass over
+// the same rows, 64 at a time: each brings 16 of them into LDS as fragments, the
+// next while the present ones are used (without LDS the waves' reads of the same
+// rows were bound by L1).  The rows of a key range are split into parts where
+// there are too few ranges; their sums go to the workspace and are added by a
+// second kernel.  Bound by the exponentials and the products.
 //
 // One tile of 16 rows: the rows stay in registers and the keys pass by, 16 at
 // a time per step and two steps ahead, 64 steps' pages looked up at once.  Bound
@@ -36,15 +37,11 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // ---------------------------------------------------------------- many rows
 
-// 16 rows and their -log2(e) lse.
-template <class Q, int D>
-struct RowTile {
-    typename Q::frag f[D / 32];
-    float lse;
-};
-
 template <class Q, int D, int KT>
 __global__ __launch_bounds__(256, 2) void kv8_weights_kernel(WeighArgs a) {
+    constexpr int KS = D / 32;
+    __shared__ u32x4 stage[2][4][KS][64];          // [buffer][16-row tile][step][lane]
+    __shared__ float stage_lse[2][64];
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const long pairs = (long)a.q.B * a.c.Hkv;
@@ -54,17 +51,17 @@ __global__ __launch_bounds__(256, 2) void kv8_weights_kernel(WeighArgs a) {
     u /= a.parts;
     const int b = (int)(pair / a.c.Hkv), kvh = (int)(pair % a.c.Hkv);
     const int len = cached_len(a.c, b);
-    const long s_first = (u * 4 + wave) * (16L * KT);
-    if (s_first >= len) return;
-    const int s0 = (int)s_first;
+    const long g_first = u * 4 * (16L * KT);       // the workgroup's first key
+    if (g_first >= len) return;
+    const int s0 = (int)min(g_first + wave * 16 * KT, (long)len);      // a wave behind the end only brings rows
     const int shift = a.c.page_shift;
 
-    typename Q::frag key[KT][D / 32];
+    typename Q::frag key[KT][KS];
     float c[KT];
     bool exists[KT];
 #pragma unroll
     for (int h = 0; h < KT; ++h) {
-        const int s = s0 + 16 * h;
+        const int s = s0 / 16 * 16 + 16 * h;
         const int nth = s >> shift;
         int pid = nth < a.c.max_pages ? a.c.table[(long)b * a.c.max_pages + nth] : -1;
         exists[h] = s < len && pid >= 0 && pid < a.c.num_pages;
@@ -80,20 +77,20 @@ __global__ __launch_bounds__(256, 2) void kv8_weights_kernel(WeighArgs a) {
         }
     }
 
-    // Rows [first, all_from) see some of the keys, [all_from, rows) all of them;
-    // rows behind the last query are left out.
+    // Rows [first, all_from) see some of the wave's keys, [all_from, rows) all of
+    // them; rows behind the last query are left out.  The workgroup starts at the
+    // first row that sees any of its keys.
     const int G = a.q.G;
     const int queries = a.q.q_lens ? min(max(a.q.q_lens[b], 0), a.q.S) : a.q.S;
     const int rows = queries * G;
-    int first = 0, all_from = 0;
-    if (a.q.q_start != nullptr) {
-        const long start = a.q.q_start[b];
-        first = (int)min(max(((long)s0 + 1) * a.q.ratio - 1 - start, 0L), (long)queries) * G;
-        all_from = (int)min(max(((long)s0 + 16 * KT) * a.q.ratio - 1 - start, 0L), (long)queries) * G;
-    }
-    if (s0 + 16 * KT > len) all_from = rows;                    // keys behind the sequence
-    const int tiles = (rows - first + 15) / 16;
-    const int per_part = (tiles + a.parts - 1) / a.parts;
+    auto sees = [&](long s) {                      // first row that sees token s
+        if (a.q.q_start == nullptr) return 0;
+        return (int)min(max((s + 1) * a.q.ratio - 1 - a.q.q_start[b], 0L), (long)queries) * G;
+    };
+    const int g_row = sees(g_first), first = s0 < len ? sees(s0) : rows;
+    const int all_from = s0 + 16 * KT > len ? rows : sees((long)s0 + 16 * KT - 1);
+    const int tiles = (rows - g_row + 15) / 16;
+    const int per_part = ((tiles + a.parts - 1) / a.parts + 3) / 4 * 4;
     const int t_lo = min(part * per_part, tiles), t_hi = min(t_lo + per_part, tiles);
 
     f32x4 sum[KT];
@@ -101,39 +98,51 @@ __global__ __launch_bounds__(256, 2) void kv8_weights_kernel(WeighArgs a) {
     for (int h = 0; h < KT; ++h) sum[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (t_lo < t_hi) {
         const typename Q::elem* q = static_cast<const typename Q::elem*>(a.q.q) + b * a.q.sb + 16 * g;
-        // query and head of this lane's row of the tile that is loaded next
-        const int r_first = first + 16 * t_lo + (lane & 15);
+        // query and head of this lane's row of the wave's next tile
+        const int r_first = g_row + 16 * (t_lo + wave) + (lane & 15);
         int t = r_first / G, h_of = r_first - t * G;
-        const int step_t = 16 / G, step_h = 16 - step_t * G;
-        auto load = [&](RowTile<Q, D>& x) {
+        const int step_t = 64 / G, step_h = 64 - step_t * G;
+        typename Q::frag held[KS];
+        float held_lse = 0.0f;
+        auto load = [&]() {
             const bool in = t < queries;
             const int tt = in ? t : queries - 1, head = kvh * G + (in ? h_of : 0);
             const typename Q::elem* at = q + tt * a.q.ss + head * a.q.sh;
 #pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks)
-                x.f[ks] = *reinterpret_cast<const typename Q::frag*>(at + 64 * (ks / 2) + 8 * (ks & 1));
-            x.lse = a.lse[((long)b * a.q.S + tt) * a.q.Hq + head];
+            for (int ks = 0; ks < KS; ++ks)
+                held[ks] = *reinterpret_cast<const typename Q::frag*>(at + 64 * (ks / 2) + 8 * (ks & 1));
+            held_lse = a.lse[((long)b * a.q.S + tt) * a.q.Hq + head];
             t += step_t;
             h_of += step_h;
             const bool wrap = h_of >= G;
             t += wrap ? 1 : 0;
             h_of -= wrap ? G : 0;
         };
-        auto add = [&](const RowTile<Q, D>& x, int i) {
+        auto store = [&](int to) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) stage[to][wave][ks][lane] = __builtin_bit_cast(u32x4, held[ks]);
+            if (lane < 16) stage_lse[to][16 * wave + lane] = held_lse;
+        };
+        auto add = [&](int from, int x, int i) {   // tile i, the x-th of the buffer
+            const int r0 = g_row + 16 * i;
+            if (r0 + 16 <= first) return;
+            typename Q::frag f[KS];
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) f[ks] = __builtin_bit_cast(typename Q::frag, stage[from][x][ks][lane]);
+            const float lse = stage_lse[from][16 * x + (lane & 15)];
             // a row whose lse is -inf gives nothing, whatever its scores are
-            const int r0 = first + 16 * i;
-            const bool edge = r0 < all_from || r0 + 16 > rows || __any(x.lse == neg_inf());
-            const float base = -x.lse * kLog2e;
+            const bool edge = r0 < all_from || r0 + 16 > rows || __any(lse == neg_inf());
+            const float base = -lse * kLog2e;
             int vis = 0;
             if (edge) {
                 const int r = r0 + (lane & 15);
-                vis = r < rows && x.lse != neg_inf() ? visible_tokens(a.q, b, r / G, len) - s0 : 0;
+                vis = r < rows && lse != neg_inf() ? visible_tokens(a.q, b, r / G, len) - s0 : 0;
             }
 #pragma unroll
             for (int h = 0; h < KT; ++h) {
                 f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int ks = 0; ks < D / 32; ++ks) y = Q::mfma(key[h][ks], x.f[ks], y);
+                for (int ks = 0; ks < KS; ++ks) y = Q::mfma(key[h][ks], f[ks], y);
                 f32x4 p;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[j], c[h], base));
@@ -146,13 +155,18 @@ __global__ __launch_bounds__(256, 2) void kv8_weights_kernel(WeighArgs a) {
                 sum[h] += p;
             }
         };
-        RowTile<Q, D> one, two;
-        load(one);
-        for (int i = t_lo; i < t_hi; i += 2) {
-            if (i + 1 < t_hi) load(two);
-            add(one, i);
-            if (i + 2 < t_hi) load(one);
-            if (i + 1 < t_hi) add(two, i + 1);
+        load();
+        store(0);
+        __syncthreads();
+        int cur = 0;
+        for (int i = t_lo; i < t_hi; i += 4) {
+            if (i + 4 < t_hi) load();
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (i + x < t_hi) add(cur, x, i + x);
+            if (i + 4 < t_hi) store(cur ^ 1);
+            __syncthreads();
+            cur ^= 1;
         }
     }
 #pragma unroll
