@@ -312,15 +312,18 @@ struct ListInfo {
     uint32_t ok[2];                    // entries that are there
 };
 
-// One query's list, 32 entries a tile, for two waves: one loads and converts
-// the keys, the other the values, two tiles ahead of the one in use (a gather
-// from L2 takes longer than a tile).  Lane e of both looks up entry e of the
+// One query's list, 32 entries a tile, for four waves of 16 heads each: two load
+// and convert the keys, the others the values, two tiles ahead of the one in use
+// (a gather from L2 takes longer than a tile).  16 heads to a wave, not 32: the
+// fragments are read from LDS twice as often, but four waves fit a SIMD instead
+// of two and cover each other's trips to LDS (@@).  Lane e of all looks up entry e of the
 // next 64: its token and page while the entries before are used, its row of the
 // cache and scales when their codes are to be loaded, so that no load waits for
 // another's address.  FAR: the pages pass 4 GiB, offsets into them take 64 bits.
 template <class Q, int D, int NT, bool FAR>
-__global__ __launch_bounds__(128, 2) void kv8_selected_tiles_kernel(AttendArgs a, AttendPlan plan) {
-    constexpr int W = 2, KT = 32, VB = D / 16;     // VB: a lane's value codes of one key
+__global__ __launch_bounds__(256, D <= 128 ? 4 : 2) void kv8_selected_tiles_kernel(AttendArgs a, AttendPlan plan) {
+    constexpr int W = 4, KT = 32, VB = D / 16;     // VB: a lane's value codes of one key
+    constexpr int VH = D <= 128 ? 1 : D / 128;     // 4-byte groups of them that a wave takes
     __shared__ Tile<D, KT> tiles[2];
     __shared__ ListInfo infos[2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -389,34 +392,29 @@ __global__ __launch_bounds__(128, 2) void kv8_selected_tiles_kernel(AttendArgs a
         };
 
         struct Codes {
-            uint32_t w[2 * VB];
+            uint32_t w[VB > 8 * VH ? VB : 8 * VH];
         };
+        const bool does_keys = wave < 2, does_values = !does_keys && (wave - 2) * VH < D / 64;
         auto load = [&](Codes& x, int e0) {        // e0: the tile's first of the 64 entries
-            if (wave == 0) {
+            if (does_keys) {
+                const uint8_t* p = row_at(a.c.k, e0 + 16 * wave + (lane & 15), 16 * g);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t* p = row_at(a.c.k, e0 + 16 * h + (lane & 15), 16 * g);
+                for (int u = 0; u < D / 64; ++u) {
+                    const u32x4 v = *reinterpret_cast<const u32x4*>(p + 64 * u);
 #pragma unroll
-                    for (int u = 0; u < D / 64; ++u) {
-                        const u32x4 v = *reinterpret_cast<const u32x4*>(p + 64 * u);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x.w[VB * h + 4 * u + i] = v[i];
-                    }
+                    for (int i = 0; i < 4; ++i) x.w[4 * u + i] = v[i];
                 }
-            } else {
+            } else if (does_values) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint8_t* p = row_at(a.c.v, e0 + 4 * g + (16 * (j / 4) + j % 4), (lane & 15) * VB);
-                    if constexpr (VB == 4) {
+                    const uint8_t* p =
+                        row_at(a.c.v, e0 + 4 * g + (16 * (j / 4) + j % 4), (lane & 15) * VB + 4 * VH * (wave - 2));
+                    if constexpr (VH == 1) {
                         x.w[j] = *reinterpret_cast<const uint32_t*>(p);
-                    } else if constexpr (VB == 8) {
+                    } else {
                         const uint2 v = *reinterpret_cast<const uint2*>(p);
                         x.w[j] = v.x;
                         x.w[8 + j] = v.y;
-                    } else {
-                        const u32x4 v = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) x.w[8 * u + j] = v[u];
                     }
                 }
             }
@@ -424,14 +422,11 @@ __global__ __launch_bounds__(128, 2) void kv8_selected_tiles_kernel(AttendArgs a
         // converts them into buffer `to`; there: which of the tile's entries are
         auto store = [&](const Codes& x, uint32_t there, int to) {
             Tile<D, KT>& t = tiles[to];
-            if (wave == 0) {
+            if (does_keys) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int ks = 0; ks < D / 32; ++ks)
-                        t.k[h][ks][lane] =
-                            __builtin_bit_cast(u32x4, key_frag<Q>(x.w[VB * h + 2 * ks], x.w[VB * h + 2 * ks + 1]));
-            } else {
+                for (int ks = 0; ks < D / 32; ++ks)
+                    t.k[wave][ks][lane] = __builtin_bit_cast(u32x4, key_frag<Q>(x.w[2 * ks], x.w[2 * ks + 1]));
+            } else if (does_values) {
                 uint32_t ok = ~0u;
                 if (there != ~0u) {
                     ok = 0;
@@ -439,7 +434,7 @@ __global__ __launch_bounds__(128, 2) void kv8_selected_tiles_kernel(AttendArgs a
                     for (int j = 0; j < 8; ++j) ok |= (there >> key_of(j, g) & 1) << j;
                 }
 #pragma unroll
-                for (int u = 0; u < D / 64; ++u) {
+                for (int u = 0; u < VH; ++u) {
                     uint32_t v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = x.w[8 * u + j];
@@ -447,7 +442,8 @@ __global__ __launch_bounds__(128, 2) void kv8_selected_tiles_kernel(AttendArgs a
                     f16x8 f[4];
                     value_frags(v, f);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) t.v[0][4 * u + e][lane] = __builtin_bit_cast(u32x4, f[e]);
+                    for (int e = 0; e < 4; ++e)
+                        t.v[0][4 * (VH * (wave - 2) + u) + e][lane] = __builtin_bit_cast(u32x4, f[e]);
                 }
             }
         };
@@ -528,7 +524,7 @@ hipError_t launch(const AttendArgs& a, const AttendPlan& plan) {
     const bool far = ((double)a.c.num_pages * a.c.Hkv * D) * (1 << a.c.page_shift) > 4294967296.0;
     if (!sel && plan.waves == 8) go(kv8_dense_tiles_kernel<Q, D, NT, 8, KT>, 8);
     else if (!sel) go(kv8_dense_tiles_kernel<Q, D, NT, 4, KT>, 4);
-    else far ? go(kv8_selected_tiles_kernel<Q, D, NT, true>, 2) : go(kv8_selected_tiles_kernel<Q, D, NT, false>, 2);
+    else far ? go(kv8_selected_tiles_kernel<Q, D, 1, true>, 4) : go(kv8_selected_tiles_kernel<Q, D, 1, false>, 4);
     return hipGetLastError();
 }
 

@@ -7,8 +7,8 @@ namespace lix {
 
 // Rows to a wave: 32 where their accumulators leave room for two waves per
 // SIMD (D <= 128) and there are more than 16, else 16.  Many rows: workgroups
-// of 8 or 4 waves that share the conversion of their keys (2 for a query's
-// heads over its list), each wave with its own rows.  Few: workgroups of 4 waves
+// of 8 or 4 waves that share the conversion of their keys, each wave with its
+// own rows (16 heads of a query over its list).  Few: workgroups of 4 waves
 // that share the rows and take turns at the keys.
 //
 // Where the rows make too few workgroups, the keys are split into parts of at
@@ -21,8 +21,12 @@ AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_p
     const long keys = topk > 0 ? topk : (long)max_pages * page;
     AttendPlan p{};
     p.tiles = rows > 16 && D <= 128 ? 2 : 1;
-    if (topk > 0) p.waves = rows <= 16 ? 0 : 2;
-    else p.waves = rows > 8 * 16 * p.tiles ? 8 : rows > 64 ? 4 : 0;
+    if (topk > 0) {
+        p.tiles = 1;
+        p.waves = rows > 16 ? 4 : 0;
+    } else {
+        p.waves = rows > 8 * 16 * p.tiles ? 8 : rows > 64 ? 4 : 0;
+    }
     const long group = 16L * p.tiles * (p.waves > 0 ? p.waves : 1);
     p.row_tiles = (int)((rows + group - 1) / group);
     p.tasks = (long)B * Hkv * (topk > 0 ? S : 1);
