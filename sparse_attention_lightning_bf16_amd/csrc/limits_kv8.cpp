@@ -12,10 +12,10 @@ namespace lix {
 // that share the rows and take turns at the keys.
 //
 // Where the rows make too few workgroups, the keys are split into parts of at
-// least 512 keys: for many rows until the card is full (2048 waves), for few
+// least 1024 keys: for many rows until the card is full (2048 waves), for few
 // until there are 1024 workgroups, two for each place on the card.
 AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pages, int topk) {
-    constexpr long kWaves = 2048, kGroups = 1024, kPartKeys = 512;
+    constexpr long kWaves = 2048, kGroups = 1024, kPartKeys = 1024;
     const int G = Hq / Hkv;
     const long rows = topk > 0 ? G : (long)S * G;
     const long keys = topk > 0 ? topk : (long)max_pages * page;
@@ -33,7 +33,7 @@ AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_p
     const long groups = p.tasks * p.row_tiles;
     const long wanted = p.waves > 0 ? kWaves / p.waves : kGroups;
     long parts = (wanted + groups - 1) / groups;
-    const long most = (keys + kPartKeys - 1) / kPartKeys;
+    const long most = keys < kPartKeys ? 1 : keys / kPartKeys;
     if (parts > most) parts = most;
     if (parts > kMaxParts) parts = kMaxParts;
     p.parts = (int)parts;

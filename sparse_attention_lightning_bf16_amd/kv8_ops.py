@@ -14,6 +14,7 @@ from . import _lib
 from .ops import _need, _ptr, _stream
 
 _DTYPES = {torch.bfloat16: _lib.LIX_BF16, torch.float16: _lib.LIX_FP16}
+_E4M3, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
 
 
 class KV8Cache(NamedTuple):
@@ -42,39 +43,49 @@ def _cache(cache, table, lens):
     """Checks a cache and its tables; the shape of the codes.  One pass of cheap tests first: the calls of a
     decoding step last about as long on the host as on the GPU."""
     k, v, ks, vs = cache
-    dev = k.get_device()
-    if not (dev >= 0 and _is(k, torch.float8_e4m3fn, 4, dev) and _is(v, torch.float8_e4m3fn, 4, dev)
-            and _is(ks, torch.float32, 2, dev) and _is(vs, torch.float32, 2, dev)
-            and _is(table, torch.int32, 2, dev) and _is(lens, torch.int32, 1, dev)):
-        _need(k, "cache.k", torch.float8_e4m3fn, 4)
-        _need(v, "cache.v", torch.float8_e4m3fn, 4)
-        _need(ks, "cache.k_scale", torch.float32, 2)
-        _need(vs, "cache.v_scale", torch.float32, 2)
-        _need(table, "block_table", torch.int32, 2)
-        _need(lens, "kv_lens", torch.int32, 1)
-        raise ValueError("the cache, block_table and kv_lens must be on the same device")
-    shape = k.shape
-    if v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
+    try:
+        dev, shape = k.get_device(), k.shape
+        ok = (dev >= 0 and k.dtype is _E4M3 and v.dtype is _E4M3 and ks.dtype is _F32 and vs.dtype is _F32
+              and table.dtype is _I32 and lens.dtype is _I32 and v.shape == shape and k.is_contiguous()
+              and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous() and table.is_contiguous()
+              and lens.is_contiguous() and v.get_device() == dev and ks.get_device() == dev
+              and vs.get_device() == dev and table.get_device() == dev and lens.get_device() == dev
+              and ks.shape == shape[:2] and vs.shape == shape[:2] and len(shape) == 4 and table.ndim == 2
+              and lens.ndim == 1 and lens.shape[0] == table.shape[0])
+    except AttributeError:
+        ok = False
+    if ok:
+        return shape
+    _need(k, "cache.k", _E4M3, 4)
+    _need(v, "cache.v", _E4M3, 4)
+    _need(ks, "cache.k_scale", _F32, 2)
+    _need(vs, "cache.v_scale", _F32, 2)
+    _need(table, "block_table", _I32, 2)
+    _need(lens, "kv_lens", _I32, 1)
+    if v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != k.shape[:2]:
         raise ValueError("the cache must hold k and v [num_pages, kv_heads, page, head_dim] and scales "
                          "[num_pages, kv_heads]")
     if lens.shape[0] != table.shape[0]:
         raise ValueError("block_table and kv_lens must have one row per sequence")
-    return shape
+    raise ValueError("the cache, block_table and kv_lens must be on the same device")
 
 
-def _rows(x, name, batch, device):
+def _rows(x, name, batch, like):
+    if (isinstance(x, torch.Tensor) and x.dtype in _DTYPES and x.ndim == 4 and x.shape[0] == batch
+            and x.get_device() == like.get_device() and not (x.requires_grad and torch.is_grad_enabled())):
+        strides = x.stride()
+        if strides[3] == 1:
+            return strides
+        raise ValueError(f"the last dimension of {name} must be contiguous")
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
         raise TypeError(f"{name} must be a bfloat16 or float16 tensor")
-    if x.dim() != 4:
+    if x.ndim != 4:
         raise ValueError(f"{name} must have 4 dimensions, got shape {tuple(x.shape)}")
-    if x.stride(3) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
     if x.shape[0] != batch:
         raise ValueError(f"{name} must have one row per sequence of block_table ({batch}), got {x.shape[0]}")
-    if x.device != device:
+    if x.device != like.device:
         raise ValueError(f"{name} must be on the cache's device")
-    if x.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name} asks for a gradient, which the 8-bit cache does not record")
+    raise ValueError(f"{name} asks for a gradient, which the 8-bit cache does not record")
 
 
 def _per_sequence(x, name, lens):
@@ -93,13 +104,11 @@ def kv8_append(cache, k, v, block_table, kv_lens, new_lens=None):
     changed.  Returns the cache."""
     pages, heads, page, dim = _cache(cache, block_table, kv_lens)
     B, mp = block_table.shape
-    _rows(k, "k", B, cache.k.device)
-    _rows(v, "v", B, cache.k.device)
+    sk, sv = _rows(k, "k", B, cache.k), _rows(v, "v", B, cache.k)
     if v.shape != k.shape or v.dtype != k.dtype or k.shape[2] != heads or k.shape[3] != dim:
         raise ValueError(f"k and v must be [{B}, S, {heads}, {dim}] of one dtype")
     st = _lib.load().lix_kv8_append(
-        k.data_ptr(), k.stride(0), k.stride(1), k.stride(2), v.data_ptr(), v.stride(0), v.stride(1), v.stride(2),
-        _DTYPES[k.dtype], B, k.shape[1], heads, dim, cache.k.data_ptr(), cache.v.data_ptr(),
+        k.data_ptr(), sk[0], sk[1], sk[2], v.data_ptr(), sv[0], sv[1], sv[2], _DTYPES[k.dtype], B, k.shape[1], heads, dim, cache.k.data_ptr(), cache.v.data_ptr(),
         cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), pages, page, block_table.data_ptr(), mp,
         kv_lens.data_ptr(), _per_sequence(new_lens, "new_lens", kv_lens), _stream(k.device))
     _lib.check(st, "lix_kv8_append")
@@ -108,11 +117,11 @@ def kv8_append(cache, k, v, block_table, kv_lens, new_lens=None):
 
 def _query(q, cache, table, lens, q_start, q_lens, scale):
     pages, heads, page, dim = _cache(cache, table, lens)
-    _rows(q, "q", table.shape[0], cache.k.device)
+    strides = _rows(q, "q", table.shape[0], cache.k)
     if q.shape[2] % heads or q.shape[3] != dim:
         raise ValueError(f"q must be [B, S, heads, {dim}] with heads a multiple of {heads}, got {tuple(q.shape)}")
-    return (pages, heads, page, dim, _per_sequence(q_start, "q_start", lens), _per_sequence(q_lens, "q_lens", lens),
-            float(dim ** -0.5 if scale is None else scale))
+    return (pages, heads, page, dim, strides, _per_sequence(q_start, "q_start", lens),
+            _per_sequence(q_lens, "q_lens", lens), float(dim ** -0.5 if scale is None else scale))
 
 
 def kv8_attention(q, cache, block_table, kv_lens, q_start=None, q_lens=None, compress_ratio=1, scale=None,
@@ -125,7 +134,7 @@ def kv8_attention(q, cache, block_table, kv_lens, q_start=None, q_lens=None, com
     heads.  scale: of the scores, head_dim ** -0.5 if None.  workspace: an optional uint8 GPU tensor of
     kv8_attention_workspace_bytes.  Returns (out like q, lse fp32 [B, S, heads]); a query that sees nothing has
     out 0 and lse -inf."""
-    pages, heads, page, dim, start, lens, scale = _query(q, cache, block_table, kv_lens, q_start, q_lens, scale)
+    pages, heads, page, dim, sq, start, lens, scale = _query(q, cache, block_table, kv_lens, q_start, q_lens, scale)
     B, S, Hq, _ = q.shape
     mp = block_table.shape[1]
     topk = 0
@@ -144,7 +153,7 @@ def kv8_attention(q, cache, block_table, kv_lens, q_start=None, q_lens=None, com
     out = torch.empty_like(q, memory_format=torch.contiguous_format)
     lse = torch.empty((B, S, Hq), dtype=torch.float32, device=q.device)
     st = lib.lix_kv8_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), _DTYPES[q.dtype], B, S, Hq, heads, dim,
+        q.data_ptr(), sq[0], sq[1], sq[2], _DTYPES[q.dtype], B, S, Hq, heads, dim,
         cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), pages, page,
         block_table.data_ptr(), mp, kv_lens.data_ptr(), start, lens, int(compress_ratio), scale, _ptr(topk_indices),
         topk, out.data_ptr(), lse.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(),
@@ -166,7 +175,7 @@ def kv8_token_weights(q, cache, block_table, kv_lens, lse, q_start=None, q_lens=
     the heads of its key head.  Arguments as for kv8_attention; lse is what it returned.  Returns fp32
     [B, kv_heads, max_pages * page]; out (of at least that width) is written for s < kv_lens[b], or added to with
     accumulate=True, and keeps its other entries."""
-    pages, heads, page, dim, start, lens, scale = _query(q, cache, block_table, kv_lens, q_start, q_lens, scale)
+    pages, heads, page, dim, sq, start, lens, scale = _query(q, cache, block_table, kv_lens, q_start, q_lens, scale)
     B, S, Hq, _ = q.shape
     mp = block_table.shape[1]
     _need(lse, "lse", torch.float32, 3)
@@ -184,7 +193,7 @@ def kv8_token_weights(q, cache, block_table, kv_lens, lse, q_start=None, q_lens=
     need = lib.lix_kv8_token_weights_workspace_bytes(B, S, Hq, heads, dim, page, mp)
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
     st = lib.lix_kv8_token_weights(
-        q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), _DTYPES[q.dtype], B, S, Hq, heads, dim,
+        q.data_ptr(), sq[0], sq[1], sq[2], _DTYPES[q.dtype], B, S, Hq, heads, dim,
         cache.k.data_ptr(), cache.k_scale.data_ptr(), pages, page, block_table.data_ptr(), mp, kv_lens.data_ptr(),
         start, lens, int(compress_ratio), scale, lse.data_ptr(), out.data_ptr(), out.shape[2], int(bool(accumulate)),
         _ptr(ws), max(need, 0), _stream(q.device))

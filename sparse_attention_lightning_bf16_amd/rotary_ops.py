@@ -71,16 +71,18 @@ def rotary_frequencies(rot, theta=10000.0, scaling=None, factor=1.0, original_ma
 
 
 def _rotate(x, positions, inv_freq, layout, start, scale, inverse, out=None):
-    heads = x.dim() == 4
-    N0, N1, D = x.shape[0], x.shape[1], x.shape[-1]
-    H = x.shape[2] if heads else 1
+    shape, strides = x.shape, x.stride()
+    N0, N1, H, sh = (*shape[:3], strides[2]) if len(shape) == 4 else (*shape[:2], 1, 0)
+    p0, p1 = positions.stride()
+    ps = positions.shape
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    st = _lib.load().lix_rotary(x.data_ptr(), x.stride(0), x.stride(1), x.stride(2) if heads else 0,
-                                positions.data_ptr(), positions.stride(0), positions.stride(1), inv_freq.data_ptr(),
-                                N0, N1, H, D, 2 * inv_freq.shape[0], start, _LAYOUTS[layout], scale, inverse,
-                                _DTYPES[x.dtype], out.data_ptr(), out.stride(0), out.stride(1),
-                                out.stride(2) if heads else 0, _stream(x.device))
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    so = out.stride()
+    st = _lib.load().lix_rotary(x.data_ptr(), strides[0], strides[1], sh, positions.data_ptr(),
+                                p0 if ps[0] == N0 else 0, p1 if ps[1] == N1 else 0, inv_freq.data_ptr(), N0, N1, H,
+                                shape[-1], 2 * inv_freq.shape[0], start, _LAYOUTS[layout], scale, inverse,
+                                _DTYPES[x.dtype], out.data_ptr(), so[0], so[1], so[2] if len(shape) == 4 else 0,
+                                _stream(x.device))
     _lib.check(st, "lix_rotary")
     return out
 
@@ -126,9 +128,8 @@ def rotary(x, positions, inv_freq, layout="half", start=0, scale=1.0, out=None):
     N0, N1 = x.shape[0], x.shape[1]
     if positions.dim() != 2 or positions.shape[0] not in (1, N0) or positions.shape[1] not in (1, N1):
         raise ValueError(f"positions must broadcast to [{N0}, {N1}], got shape {tuple(positions.shape)}")
-    positions = positions.expand(N0, N1)
     _need(inv_freq, "inv_freq", torch.float64, 1)
-    if positions.device != x.device or inv_freq.device != x.device:
+    if positions.get_device() != x.get_device() or inv_freq.get_device() != x.get_device():
         raise ValueError("x, positions and inv_freq must be on the same device")
     if layout not in _LAYOUTS:
         raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")

@@ -141,7 +141,7 @@ def test_workspace_sizes():
     f = lx.kv8_attention_workspace_bytes
     assert f(2, 4096, 32, 4, 128, 64, 128) == 0              # rows enough to fill the card: not split
     assert f(1, 1, 8, 1, 128, 64, 1) == 0                    # one part's worth of keys
-    for args in ((1, 1, 8, 1, 128, 64, 512), (1, 1, 64, 1, 256, 16, 512, 2000)):
+    for args in ((1, 1, 8, 1, 128, 64, 512), (1, 1, 64, 1, 256, 16, 512, 4000)):
         need = f(*args)
         rows = args[2]
         assert need > 0 and need % (rows * (args[4] + 2) * 4) == 0
