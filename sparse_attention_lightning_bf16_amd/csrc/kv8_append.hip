@@ -34,7 +34,7 @@ __device__ __forceinline__ void unpack8(const u32x4& w, float (&x)[8]) {
 // tokens may fall on).  CH: pieces of 8 values a thread holds at most.
 template <class T, int CH>
 __global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a, int pages) {
-    __shared__ float part[4];
+    __shared__ float part[2][4];
     const int j = blockIdx.x % pages;
     int rest = blockIdx.x / pages;
     const int which = rest & 1;
@@ -76,9 +76,22 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a, int 
         float f[8];
         unpack8<T>(raw[c], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = finite_top(top, f[e]);
+        for (int e = 0; e < 8; e += 2) top = fmaxf(top, fmaxf(fabsf(f[e]), fabsf(f[e + 1])));     // NaN is passed over
     }
-    top = workgroup_max(top, part);
+    top = workgroup_max(top, part[0]);
+    // Rare: infinities, which do not count for the scale and saturate.
+    const bool infinite = top == kInf;
+    if (infinite) {
+        top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            float f[8];
+            unpack8<T>(raw[c], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = finite_top(top, f[e]);
+        }
+        top = workgroup_max(top, part[1]);
+    }
 
     const long at = (long)pid * a.c.Hkv + h;
     float* scale_at = (which ? a.c.v_scale : a.c.k_scale) + at;
@@ -94,7 +107,7 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a, int 
                 e4m3_quad_to_f32(*w, f);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) f[e] = f[e] * before / scale;
-                *w = e4m3_quad(f);
+                *w = e4m3_quad<true>(f);
             }
         }
         __syncthreads();                              // every thread has read the old scale
@@ -104,7 +117,7 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a, int 
     // exact.  Another one, of a page with older tokens, takes a division.
     const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0 && scale >= 0x1p-120f && scale <= 0x1p120f;
     const float inv = exact ? 1.0f / scale : 1.0f, by = exact ? 1.0f : scale;
-    auto write = [&](auto divide) {
+    auto write = [&](auto general) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int i = c * kThreads + threadIdx.x;
@@ -112,14 +125,14 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a, int 
                 float f[8];
                 unpack8<T>(raw[c], f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = divide ? f[e] / by : f[e] * inv;
+                for (int e = 0; e < 8; ++e) f[e] = general ? f[e] / by * inv : f[e] * inv;
                 const float lo4[4] = {f[0], f[1], f[2], f[3]}, hi4[4] = {f[4], f[5], f[6], f[7]};
-                const uint2 w = make_uint2(e4m3_quad(lo4), e4m3_quad(hi4));
+                const uint2 w = make_uint2(e4m3_quad<general>(lo4), e4m3_quad<general>(hi4));
                 *reinterpret_cast<uint2*>(codes + (long)first * D + i * 8) = w;
             }
         }
     };
-    if (exact) write(std::false_type{});
+    if (exact && !infinite) write(std::false_type{});
     else write(std::true_type{});
 }
 
@@ -417,8 +430,10 @@ __global__ __launch_bounds__(kThreads) void kv8_move_kernel(EvictArgs a, int pag
 
     const int per_row = D >> 4;                       // pieces of 16 codes
     const int pieces = here * per_row;
+    // the largest code of a row is found first, its scale multiplied once
     u32x4 raw[2][CH];
     float scales[2][CH], top[2] = {0.0f, 0.0f};
+    bool infinite = false;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int i = c * kThreads + threadIdx.x;
@@ -435,14 +450,17 @@ __global__ __launch_bounds__(kThreads) void kv8_move_kernel(EvictArgs a, int pag
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < CH; ++c) {
+            float most = 0.0f;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 float f[4];
                 e4m3_quad_to_f32(raw[x][c][w], f);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top[x] = finite_top(top[x], f[e] * scales[x][c]);
+                most = fmaxf(fmaxf(most, fmaxf(fabsf(f[0]), fabsf(f[1]))), fmaxf(fabsf(f[2]), fabsf(f[3])));   // no NaN
             }
+            top[x] = finite_top(top[x], most * scales[x][c]);
+            infinite |= !(fabsf(scales[x][c] * kE4M3Max) < kInf);
+        }
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) top[x] = fmaxf(top[x], __shfl_xor(top[x], o));
         if ((threadIdx.x & 63) == 0) part[x][threadIdx.x >> 6] = top[x];
@@ -452,26 +470,32 @@ __global__ __launch_bounds__(kThreads) void kv8_move_kernel(EvictArgs a, int pag
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const float scale = page_scale(fmaxf(fmaxf(part[x][0], part[x][1]), fmaxf(part[x][2], part[x][3])));
-        // the new scale is a power of two: its reciprocal is exact
-        const float inv = 1.0f / scale;
         if (threadIdx.x == 0) (x ? a.c.v_scale : a.c.k_scale)[to] = scale;
         uint8_t* codes = (x ? a.c.v : a.c.k) + ((to * D) << shift);
+        // the new scale is a power of two: dividing by it is exact, before or after
+        // the product with the code
+        const float inv = 1.0f / scale;
+        auto write = [&](auto saturate) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int i = c * kThreads + threadIdx.x;
-            if (i < pieces) {
-                u32x4 o;
+            for (int c = 0; c < CH; ++c) {
+                const int i = c * kThreads + threadIdx.x;
+                if (i < pieces) {
+                    const float by = saturate ? scales[x][c] : scales[x][c] * inv, then = saturate ? inv : 1.0f;
+                    u32x4 o;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    float f[4];
-                    e4m3_quad_to_f32(raw[x][c][w], f);
+                    for (int w = 0; w < 4; ++w) {
+                        float f[4];
+                        e4m3_quad_to_f32(raw[x][c][w], f);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) f[e] = f[e] * scales[x][c] * inv;
-                    o[w] = e4m3_quad(f);
+                        for (int e = 0; e < 4; ++e) f[e] = f[e] * by * then;
+                        o[w] = e4m3_quad<saturate>(f);
+                    }
+                    *reinterpret_cast<u32x4*>(codes + (long)i * 16) = o;
                 }
-                *reinterpret_cast<u32x4*>(codes + (long)i * 16) = o;
             }
-        }
+        };
+        if (__any(infinite)) write(std::true_type{});
+        else write(std::false_type{});
     }
 }
 

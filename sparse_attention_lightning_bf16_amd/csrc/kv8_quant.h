@@ -18,12 +18,16 @@ __device__ __forceinline__ float page_scale(float top) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Four values as e4m3 bytes: round to nearest even, saturating; NaN stays NaN.
+// Four values as e4m3 bytes, rounded to nearest even; NaN stays NaN.  SATURATE:
+// values beyond 448 become 448; without it they have to be within.
+template <bool SATURATE>
 __device__ __forceinline__ uint32_t e4m3_quad(const float (&x)[4]) {
     float y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        y[i] = x[i] > kE4M3Max ? kE4M3Max : x[i] < -kE4M3Max ? -kE4M3Max : x[i];     // NaN compares false twice
+    for (int i = 0; i < 4; ++i) {
+        y[i] = x[i];
+        if (SATURATE) y[i] = y[i] > kE4M3Max ? kE4M3Max : y[i] < -kE4M3Max ? -kE4M3Max : y[i];   // NaN compares false
+    }
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
     w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
     return (uint32_t)w;
@@ -40,13 +44,16 @@ __device__ __forceinline__ void e4m3_quad_to_f32(uint32_t w, float (&x)[4]) {
     x[3] = hi.y;
 }
 
+constexpr float kInf = __builtin_inff();
+
 // max(top, |x|) over finite x: infinities and NaN leave top as it is.
 __device__ __forceinline__ float finite_top(float top, float x) {
     const float m = fabsf(x);
-    return m < __uint_as_float(0x7f800000u) ? fmaxf(top, m) : top;
+    return m < kInf ? fmaxf(top, m) : top;
 }
 
-// Maximum over the 256 threads of a workgroup; `part` holds 4 floats of LDS.
+// Maximum over the 256 threads of a workgroup; `part` holds 4 floats of LDS
+// that no thread is still reading.
 __device__ __forceinline__ float workgroup_max(float v, float* part) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));

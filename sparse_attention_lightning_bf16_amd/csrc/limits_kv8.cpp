@@ -43,7 +43,7 @@ AttendPlan attend_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_p
 
 // One tile of rows: ranges of 1024 keys to a wave (64 lookups of 16), shorter
 // ones down to 64 where that leaves fewer than 8192 waves.  More rows: 256 keys
-// (128 for D = 256) to a workgroup, the rows in parts until there are 1024
+// (128 for D = 256) to a workgroup, the rows in parts until there are 2048
 // workgroups, at least eight tiles of 16 rows to a part.
 WeighPlan weigh_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pages) {
     const long cap = (long)max_pages * page, pairs = (long)B * Hkv, rows = (long)S * (Hq / Hkv);
@@ -56,7 +56,7 @@ WeighPlan weigh_plan(int B, int S, int Hq, int Hkv, int D, int page, int max_pag
     }
     const long keys = D <= 128 ? 256 : 128;
     const long groups = pairs * ((cap + keys - 1) / keys);
-    long parts = (1024 + groups - 1) / groups;
+    long parts = (2048 + groups - 1) / groups;
     const long most = (rows + 127) / 128;
     if (parts > most) parts = most;
     p.parts = (int)parts;

@@ -409,6 +409,8 @@ def test_evict_matches_oracle(B, H, D, page, lens, keep, recent, sinks, ties):
     w = np.exp(g.normal(0, 2, (B, H, mp * page + 3))).astype(np.float32)
     if ties:
         w = np.round(w)
+    cache["v"][table[0, 0], 0, 0, 5:9] = [0x7F, 0xFF, 0x7E, 0xFE]      # NaN stays, and counts for no scale
+    cache["k_scale"][table[0, 0], 0] = 0.0
     dev = kc.to_device(lx, cache, DEV)
     new_lens, kept, new_w = lx.kv8_evict(dev, torch.from_numpy(table).to(DEV), kc.ints(lens, DEV),
                                          torch.from_numpy(w).to(DEV), torch.from_numpy(new_table).to(DEV), keep,
@@ -421,8 +423,8 @@ def test_evict_matches_oracle(B, H, D, page, lens, keep, recent, sinks, ties):
     assert np.array_equal(new_w.cpu().numpy(), rw)
     for x in ("k", "v"):
         got, ref = getattr(dev, x).view(torch.uint8).cpu().numpy(), want[x]
-        zero = (got & 0x7F == 0) & (ref & 0x7F == 0)
-        assert np.array_equal(got[~zero], ref[~zero]), x
+        same = ((got & 0x7F == 0) & (ref & 0x7F == 0)) | ((got & 0x7F == 0x7F) & (ref & 0x7F == 0x7F))
+        assert np.array_equal(got[~same], ref[~same]), x
         assert np.array_equal(getattr(dev, x + "_scale").cpu().numpy().astype(np.float64), want[x + "_scale"]), x
 
 
@@ -587,7 +589,8 @@ def test_refusals_on_the_device():
     with pytest.raises(lx.LixError):
         lx.kv8_attention(q, cache, table, lens, scale=float("nan"))
     with pytest.raises(lx.LixError):
-        lx.kv8_attention(q, cache, table, lens, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        wide = torch.full((2, 64), -1, dtype=torch.int32, device=DEV)      # 4096 tokens: more than one part
+        lx.kv8_attention(q, cache, wide, lens, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError):
         lx.kv8_attention(q.clone().requires_grad_(), cache, table, lens)
     with pytest.raises(ValueError):
