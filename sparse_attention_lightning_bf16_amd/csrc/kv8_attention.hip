@@ -190,7 +190,6 @@ __global__ __launch_bounds__(256, 2) void kv8_dense_kernel(AttendArgs a, AttendP
                 sc.inv[h] = lane_of(inv);
             }
             uint32_t ok = ~0u;
-            bool nans = false;
             int left[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) left[n] = vis[n] - s0;
@@ -198,9 +197,18 @@ __global__ __launch_bounds__(256, 2) void kv8_dense_kernel(AttendArgs a, AttendP
                 ok = 0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ok |= (there >> (j / 4) & 1) && s0 + key_of(j, g) < hi ? 1u << j : 0u;
-                nans = clear_hidden(raw, ok);
+                if (clear_hidden(raw, ok)) {
+                    mark_nans<Q, D, NT, 2>(w, [&](int, int u, uint32_t (&v)[8]) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = raw.v[u][j];
+                    }, left, ok);
+#pragma unroll
+                    for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) raw.v[u][j] = without_nans(raw.v[u][j]);
+                }
             }
-            step<Q, D, NT, 2, false>(w, OwnKeys<Q, D>{raw}, sc, edge, left, ok, nans);
+            step<Q, D, NT, 2, false>(w, OwnKeys<Q, D>{raw}, sc, edge, left, ok);
         };
 
         const int turns = (hi - first + kTurn - 1) / kTurn;
@@ -328,7 +336,7 @@ __global__ __launch_bounds__(256, 2) void kv8_selected_kernel(AttendArgs a, Atte
                 clear_hidden(raw, ok);             // all rows see the same keys: no NaN to keep from any
             }
             const int none[1] = {};
-            step<Q, D, 1, 2, true>(w, OwnKeys<Q, D>{raw}, sc, there != ~0u, none, ok, false);
+            step<Q, D, 1, 2, true>(w, OwnKeys<Q, D>{raw}, sc, there != ~0u, none, ok);
         };
 
         const int turns = (hi - first + kTurn - 1) / kTurn;

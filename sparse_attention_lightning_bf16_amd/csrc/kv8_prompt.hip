@@ -24,6 +24,7 @@ struct Tile {
 // Fragments of a tile's keys from LDS.
 template <class Q, int D, int KT>
 struct SharedKeys {
+    static constexpr bool kShared = true;
     const Tile<D, KT>& t;
     int first;                         // 16-key tile it starts at
     int lane;
@@ -76,14 +77,16 @@ __device__ __forceinline__ void store_unit(Tile<D, KT>& t, const Share<D, KT, W>
 }
 
 // Clears the value codes of a unit's hidden keys (bits j of ok: key 16 (j / 4)
-// + 4 g + j % 4 of the 32 is there); whether a NaN code is left.
-template <int WORDS>
+// + 4 g + j % 4 of the 32 is there) and, with NANS, its NaN codes; whether
+// there were any.
+template <bool NANS, int WORDS>
 __device__ __forceinline__ bool clear_unit(uint32_t (&w)[WORDS], uint32_t ok) {
     uint32_t bad = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         w[j] = ok >> j & 1 ? w[j] : 0u;
         bad |= nan_codes(w[j]);
+        if (NANS) w[j] = without_nans(w[j]);
     }
     return __any(bad != 0);
 }
@@ -244,7 +247,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_dense_tiles_kernel(AttendArgs a
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         ok |= (there >> (2 * p + j / 4) & 1) && s0 + 32 * p + key_of(j, g) < hi ? 1u << j : 0u;
-                    nans |= clear_unit(share.w[i], ok);
+                    nans |= clear_unit<true>(share.w[i], ok);
                 }
                 store_unit<Q>(tiles[to], share, i, unit, lane);
             }
@@ -279,7 +282,6 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_dense_tiles_kernel(AttendArgs a
                     sc.inv[h] = lane_of(inv);
                 }
                 uint32_t ok = ~0u;
-                bool nans = false;
                 int left[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) left[n] = vis[n] - s0;
@@ -288,10 +290,30 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_dense_tiles_kernel(AttendArgs a
 #pragma unroll
                     for (int j = 0; j < 4 * E; ++j)
                         ok |= (there >> (j / 4) & 1) && s0 + key_of(j, g) < hi ? 1u << j : 0u;
+                }
+                if (there != (1u << E) - 1 || s0 + KT > group_least || s0 + KT > hi) {
+                    // an edge for some wave of the workgroup: NaN codes are out of it
+                    bool nans = false;
 #pragma unroll
                     for (int i = 0; i < W; ++i) nans |= nan_at[cur][i] != 0;
+                    if (nans) {
+                        auto codes = [&](int q, int u, uint32_t (&v)[8]) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int s = s0 + 32 * q + key_of(j, g);
+                                const int pid = s < hi ? table[s >> shift] : -1;
+                                const bool is = pid >= 0 && pid < a.c.num_pages;
+                                const long at =
+                                    (((long)(is ? pid : 0) * a.c.Hkv + k.kvh) << shift) + (s & ((1 << shift) - 1));
+                                v[j] = is ? *reinterpret_cast<const uint32_t*>(a.c.v + at * D + (lane & 15) * (D / 16) +
+                                                                               4 * u)
+                                          : 0u;
+                            }
+                        };
+                        mark_nans<Q, D, NT, E>(w, codes, left, ok);
+                    }
                 }
-                step<Q, D, NT, E, false>(w, SharedKeys<Q, D, KT>{tiles[cur], 0, lane}, sc, edge, left, ok, nans);
+                step<Q, D, NT, E, false>(w, SharedKeys<Q, D, KT>{tiles[cur], 0, lane}, sc, edge, left, ok);
             }
             if (more) store(s0 + KT, next * E, cur ^ 1);
             __syncthreads();
@@ -438,7 +460,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 4 : 2) void kv8_selected_tiles_kern
                     uint32_t v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = x.w[8 * u + j];
-                    if (there != ~0u) clear_unit(v, ok);
+                    if (there != ~0u) clear_unit<false>(v, ok);
                     f16x8 f[4];
                     value_frags(v, f);
 #pragma unroll
@@ -471,7 +493,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 4 : 2) void kv8_selected_tiles_kern
                 for (int j = 0; j < 8; ++j) ok |= (there >> key_of(j, g) & 1) << j;
             }
             const int none[NT] = {};
-            step<Q, D, NT, 2, true>(w, SharedKeys<Q, D, KT>{tiles[i & 1], 0, lane}, sc, there != ~0u, none, ok, false);
+            step<Q, D, NT, 2, true>(w, SharedKeys<Q, D, KT>{tiles[i & 1], 0, lane}, sc, there != ~0u, none, ok);
         };
 
         // Even tiles pass through `even`, odd ones through `odd`; tile i is used

@@ -110,6 +110,7 @@ __device__ __forceinline__ void dense_ratio(float v_scale, float ref, float& log
 // Fragments of 32 keys from a wave's own registers.
 template <class Q, int D>
 struct OwnKeys {
+    static constexpr bool kShared = false;
     const Raw<D>& raw;
     __device__ __forceinline__ typename Q::frag key(int h, int ks) const {
         const u32x4 w = raw.k[h][ks / 2];
@@ -121,18 +122,58 @@ struct OwnKeys {
 // Key of this lane's slot j = 4 h + i, counted from the first: 16 h + 4 g + i.
 __device__ __forceinline__ int key_of(int j, int g) { return 16 * (j / 4) + 4 * g + j % 4; }
 
+// Rare: a NaN among the values of keys that not every row sees.  The products
+// are taken without it (0 in its place), and the outputs of the rows that see
+// its key become NaN here: 1 where a value is NaN times 1 where a row sees the
+// key.  words(q, u, v): the eight codes' words of 32-key group q, as Raw::v.
+template <class Q, int D, int NT, int KH, class Words>
+__device__ __forceinline__ void mark_nans(Rows<Q, D, NT>& w, const Words& words, const int (&vis)[NT], uint32_t ok) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll 1
+    for (int q = 0; q < KH / 2; ++q)
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {
+            __builtin_amdgcn_sched_barrier(0);
+            uint32_t v[8];
+            words(q, u, v);
+            f16x8 seen[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    seen[n][j] = (ok >> (8 * q + j) & 1) && 32 * q + key_of(j, g) < vis[n] ? (_Float16)1.0f
+                                                                                          : (_Float16)0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f16x8 bad;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t byte = v[j] >> (8 * e) & 0x7fu;
+                    bad[j] = byte == 0x7fu ? (_Float16)1.0f : (_Float16)0.0f;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const f32x4 hit = QFp16::mfma(bad, seen[n], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (hit[i] > 0.0f) w.acc[4 * u + e][n][i] = __uint_as_float(0x7fc00000u);
+                }
+            }
+        }
+}
+
 // One pass over KH tiles of 16 keys.  edge (uniform): some key is hidden from
-// some row; ok is then a mask of this lane's 4 KH keys that exist at all,
-// vis[n] the number of keys that the row sees, counted from the first (dense),
-// and nans (uniform) tells of a NaN among the values' codes.  Codes of keys
-// that no row sees are zero already.
+// some row; ok is then a mask of this lane's 4 KH keys that exist at all, and
+// vis[n] the number of keys that the row sees, counted from the first (dense).
+// Codes of keys that no row sees are zero already, and so are NaN codes of
+// keys that some rows do not see (mark_nans).
 //
 // All scores first, then one test whether any of them passes its row's
 // maximum, then all weights: the products of a row tile are in flight while
 // the weights of another are taken.
 template <class Q, int D, int NT, int KH, bool SEL, class Src>
 __device__ __forceinline__ void step(Rows<Q, D, NT>& w, const Src& src, const Scales<KH, SEL>& sc, bool edge,
-                                     const int (&vis)[NT], uint32_t ok, bool nans) {
+                                     const int (&vis)[NT], uint32_t ok) {
     constexpr int KS = D / 32;
     const int g = (threadIdx.x & 63) >> 4;
     f32x4 s[KH][NT];
@@ -148,6 +189,11 @@ __device__ __forceinline__ void step(Rows<Q, D, NT>& w, const Src& src, const Sc
         }
     }
 
+    // Operands out of LDS: both products are scheduled as loads and matrix
+    // instructions in turns, which keeps the next operands ahead (4096 rows of two
+    // sequences up to 8192 long, 32 heads: 860 us without, 785 with; 797 with wave
+    // priorities instead).
+    if constexpr (Src::kShared) __builtin_amdgcn_iglp_opt(1);
     constexpr int CS = SEL ? 4 * KH : KH;
     float c[CS];                       // what is left to multiply the scores with
 #pragma unroll
@@ -233,40 +279,13 @@ __device__ __forceinline__ void step(Rows<Q, D, NT>& w, const Src& src, const Sc
             }
         }
 
+    if constexpr (Src::kShared) __builtin_amdgcn_iglp_opt(1);
 #pragma unroll
     for (int q = 0; q < KH / 2; ++q)
 #pragma unroll
         for (int u = 0; u < D / 64; ++u) {
             f16x8 f[4];
             src.values(q, u, f);
-            if (edge && nans) {
-                // rare: 1 where a value is NaN times 1 where a row sees its key
-                int here = g;
-                asm volatile("" : "+v"(here), "+v"(ok));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f16x8 bad;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const bool is = f[e][j] != f[e][j];
-                        bad[j] = is ? (_Float16)1.0f : (_Float16)0.0f;
-                        f[e][j] = is ? (_Float16)0.0f : f[e][j];
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        f16x8 seen;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            seen[j] = (ok >> (8 * q + j) & 1) && (SEL || key_of(8 * q + j, here) < vis[n])
-                                          ? (_Float16)1.0f
-                                          : (_Float16)0.0f;
-                        const f32x4 hit = QFp16::mfma(bad, seen, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (hit[i] > 0.0f) w.acc[4 * u + e][n][i] = __uint_as_float(0x7fc00000u);
-                    }
-                }
-            }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -277,6 +296,9 @@ __device__ __forceinline__ void step(Rows<Q, D, NT>& w, const Src& src, const Sc
                 }
         }
 }
+
+// w with its NaN codes as zeros.
+__device__ __forceinline__ uint32_t without_nans(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xffu); }
 
 // Clears the value codes of keys that are not there (bits of ok); whether a
 // NaN code is left.
